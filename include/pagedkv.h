@@ -66,6 +66,8 @@ typedef enum {
 typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_F16 = 2 } pkv_dtype;
 
 /* Flags for the device calls. */
+/* paged_kv_append(_q4): rotate neighbouring channels (2i, 2i+1) instead of halves (i, i + rot_dim/2) */
+#define PKV_ROPE_INTERLEAVED 0x10u
 #define PKV_CHECK_BOUNDS 0x1u  /* validate device metadata in the kernels */
 #define PKV_FORCE_SIMT 0x2u    /* attention: use the CUDA-core kernel even for bf16/f16 */
 #define PKV_NO_SPLIT 0x4u      /* attention: never split the key range */
@@ -88,6 +90,8 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_F16 = 2 } pkv_dtype;
 #define PKV_DEVERR_QUERY 0x8u     /* query_start_loc not monotone, or Sq > max_query_len */
 #define PKV_DEVERR_SEGMENT 0x10u  /* a segment outside the row's query range, or a query row no segment covers */
 #define PKV_DEVERR_TIMEOUT 0x20u  /* a pipeline wait inside a kernel gave up (the kernel unwound; results invalid) */
+
+#define PKV_DEVERR_POSITION 0x40u /* a position outside [0, max_position) */
 
 /*
  * One piece of a piecewise causal/full mask, in GLOBAL key coordinates
@@ -243,6 +247,97 @@ PKV_API pkv_status paged_kv_gather(const void* key_pool, const void* value_pool,
                                    uint32_t flags, void* stream);
 
 /*
+ * paged_kv_append -- rotate a step's Q and K by position and scatter K and V into the pools, in one launch.
+ * (The pages append with paged_kv_write after a rotation of the caller's; this is the serving form.)
+ * For token t at position p = positions[t], with (c_i, s_i) = (cos_sin[p][i], cos_sin[p][rot_dim/2 + i]):
+ *   halves (default):      y[i] = x[i] c_i - x[i + rot_dim/2] s_i,  y[i + rot_dim/2] = x[i + rot_dim/2] c_i + x[i] s_i
+ *   PKV_ROPE_INTERLEAVED:  the same on the pairs x[2i], x[2i + 1]
+ * for i < rot_dim/2; channels from rot_dim on are copied.  Each product and sum is rounded to fp32 and the result
+ * once to dt.  q_out[t] = rotated q[t]; key_pool[slot] = rotated k[t]; value_pool[slot] = v[t], bit for bit.
+ *   q, k, v       device; token t's heads start at q + t * q_stride (elements; k, v likewise), [H, D] contiguous
+ *                 inside, so slices of one projection's output need no copy.  q and q_out may be NULL with Hq == 0.
+ *   positions     device int32 [T]; cos_sin device fp32 [max_position, rot_dim].  Neither is read (NULL is fine)
+ *                 when rot_dim is 0.
+ *   slot_mapping  device int64 [T]; a negative slot skips the token's K and V (q_out is still written); slots
+ *                 must be distinct (duplicates race)
+ *   q_out         device [T, Hq, D] contiguous; may be q itself when q_stride == Hq * D, else must not overlap
+ *   key_pool, value_pool  device [num_slots, Hkv, D]
+ * Supported: D in {64, 128}; rot_dim in [0, D], a multiple of 16; 16-byte aligned pointers and token strides.
+ * PKV_CHECK_BOUNDS: a slot >= num_slots is flagged and the token's K and V skipped; a position outside
+ * [0, max_position) is flagged (PKV_DEVERR_POSITION) and nothing of the token is written.
+ * T == 0 is a no-op.
+ */
+PKV_API pkv_status paged_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                   int64_t v_stride, const int32_t* positions, const float* cos_sin,
+                                   int64_t max_position, int rot_dim, const int64_t* slot_mapping, int64_t T, int Hq,
+                                   void* q_out, void* key_pool, void* value_pool, int64_t num_slots, int Hkv, int D,
+                                   pkv_dtype dt, uint32_t flags, void* stream);
+
+/*
+ * The 4-bit pool: uint8 [num_blocks, Hkv, pkv_q4_block_bytes(D)], one record per (block, head), 5 bits a value:
+ *   codes   [16 tokens][D / 2 bytes]: channel c of a token in byte c / 2, even channels in the low nibble
+ *   pairs   [16 tokens][D / 32 groups] x (fp16 step, fp16 low)
+ * A code n of a group of 32 channels stands for the fp16 number nearest to step * n + low.
+ * Quantising a group x (fp32, clamped to +-32768): low = fp16(min x), step = fp16((max x - min x) * (1/15)),
+ * n = round_half_even((x - low) * (1 / step)) clamped to [0, 15]; 0 when step is 0.  A group that holds a NaN or an
+ * infinity is stored with a NaN pair and reads back as NaN throughout.
+ */
+
+/* pkv_q4_block_bytes -- bytes of one record (10 * D); 0 when D is not 64 or 128. */
+PKV_API size_t pkv_q4_block_bytes(int D);
+
+/*
+ * paged_kv_append_q4 -- paged_kv_append into 4-bit pools: K is quantised from its unrounded fp32 rotation, V from
+ * its input values.  Arguments as there; pools of num_blocks records per head, slots in [0, num_blocks * 16).
+ */
+PKV_API pkv_status paged_kv_append_q4(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                      int64_t v_stride, const int32_t* positions, const float* cos_sin,
+                                      int64_t max_position, int rot_dim, const int64_t* slot_mapping, int64_t T,
+                                      int Hq, void* q_out, void* key_pool, void* value_pool, int64_t num_blocks,
+                                      int Hkv, int D, pkv_dtype dt, uint32_t flags, void* stream);
+
+/*
+ * paged_kv_gather_q4 -- paged_kv_gather from 4-bit pools: the values of the listed blocks, rounded to dt, in
+ * contiguous staging buffers (for paged_attn_varlen with PKV_CONTIGUOUS_KV, or to inspect a cache).
+ * Arguments and errors as paged_kv_gather; dt is the staging buffers' type.
+ */
+PKV_API pkv_status paged_kv_gather_q4(const void* key_pool, const void* value_pool, int64_t num_blocks,
+                                      const int32_t* block_table, int B, int W, int first_block, int n_blocks,
+                                      void* stage_k, void* stage_v, int64_t stage_rows, int Hkv, int D, pkv_dtype dt,
+                                      uint32_t flags, void* stream);
+
+/*
+ * paged_attn_window -- causal varlen attention through a block table, with a sliding window and attention sinks
+ * per query.  Row b's query i (of Sq) sits at p = L - Sq + i and sees key j when
+ *   0 <= j <= p   and   (window == 0  or  j < sinks  or  p - j < window).
+ * window == 0: no window (sinks then change nothing).  A query that sees no key (p < 0: L < Sq, or L == 0) gets 0.
+ * Table entries of blocks that no query of the row sees are not read: evicted blocks may hold any id.  Keys and
+ * values that no query of the row sees do not enter any output, whatever they hold; a NaN or an infinity in a
+ * value that some query of the row sees may also reach the row's other queries.
+ * One launch, no workspace: CTAs that share a query tile's keys form a cluster and merge through its shared memory.
+ * Out rows past query_start_loc[B] are left as they are.
+ *   window, sinks  >= 0
+ *   softmax_scale  finite; > 0 for bf16/f16 unless flags holds PKV_FORCE_SIMT
+ *   flags          PKV_CHECK_BOUNDS (bad block ids, query lengths, key lengths past the table or max_seq_len),
+ *                  PKV_FORCE_SIMT (the fp32 CUDA-core kernel); others are ignored
+ * Everything else as paged_attn_varlen; max_query_len may exceed max_seq_len.
+ */
+PKV_API pkv_status paged_attn_window(const void* q, int64_t Tq, int Hq, const void* key_pool, const void* value_pool,
+                                     int64_t num_blocks, int block_size, int Hkv, int D, pkv_dtype dt,
+                                     const int32_t* block_table, int B, int W, const int32_t* query_start_loc,
+                                     const int32_t* seq_lens, int max_query_len, int max_seq_len, float softmax_scale,
+                                     int window, int sinks, void* out, uint32_t flags, void* stream);
+
+/*
+ * paged_attn_q4 -- paged_attn_window over 4-bit pools; dt is q's and out's type.
+ */
+PKV_API pkv_status paged_attn_q4(const void* q, int64_t Tq, int Hq, const void* key_pool, const void* value_pool,
+                                 int64_t num_blocks, int block_size, int Hkv, int D, pkv_dtype dt,
+                                 const int32_t* block_table, int B, int W, const int32_t* query_start_loc,
+                                 const int32_t* seq_lens, int max_query_len, int max_seq_len, float softmax_scale,
+                                 int window, int sinks, void* out, uint32_t flags, void* stream);
+
+/*
  * paged_attn_workspace_size -- bytes of workspace paged_attn_varlen may use
  * for a call with these sizes (split-KV partial outputs and log-sum-exps):
  * the key-range splits the call would plan for these sizes on the current
@@ -350,7 +445,8 @@ PKV_API pkv_status pkv_check(void* stream, uint32_t* bits);
 /*
  * pkv_last_launches -- number of kernels the last device call on this thread
  * (paged_kv_write, paged_kv_gather, paged_attn_varlen, paged_kv_write_attn,
- * paged_attn_varlen_noalloc, pkv_selftest_wait) launched: 0 when it launched nothing, 2 for an
+ * paged_attn_varlen_noalloc, paged_kv_append(_q4), paged_kv_gather_q4, paged_attn_window,
+ * paged_attn_q4, pkv_selftest_wait) launched: 0 when it launched nothing, 2 for an
  * attention call that split (the attention and its combine).
  */
 PKV_API int pkv_last_launches(void);

@@ -14,7 +14,10 @@ with the CUDA path:
 * ``oracle.window``    -- the sink + recent visible-window block selection,
   the fixed table width and the padded block-table row.
 
-Every function says which page and which function on it it follows.  Parity
+* ``oracle.serving``   -- rotary append, the 4-bit pool format and causal attention with a sliding
+  window and sinks, from their formulas.
+
+Every function of the first two says which page and which function on it it follows.  Parity
 pins (tests/test_oracle_*.py) tie each function to something other than itself:
 brute force, closed forms, a library attention routine, and worked values from
 the pages' own tests.

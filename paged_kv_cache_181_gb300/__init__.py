@@ -2,7 +2,8 @@
 
 The product is ``libpagedkv.so`` (C ABI in include/pagedkv.h): a slot-mapping
 KV write, a varlen paged attention with a piecewise causal/full mask (tcgen05
-tensor cores for bf16/f16, CUDA cores for fp32), a split-KV combine, and the
+tensor cores for bf16/f16, CUDA cores for fp32), a split-KV combine, the serving
+operators (rotary append, 4-bit pools, sliding-window attention with sinks), and the
 host metadata (segments, visible window, block table, slot mapping).  This
 package is a thin ctypes binding over it.  The binding loads on first use of
 an operation, and fails loudly when the library has not been built; the
@@ -12,7 +13,8 @@ workload shapes (``configs``) and seeded draws (``synth``) need no library.
 _API = (
     "PKV_BF16", "PKV_CHECK_BOUNDS", "PKV_F16", "PKV_F32", "PKV_FORCE_SIMT", "PKV_NO_SPLIT", "PKV_SEG_CAUSAL",
     "PKV_SEG_FULL", "PKV_SPLITS", "PkvError", "block_table_row", "build_segments", "check", "last_error",
-    "paged_attn_varlen", "paged_kv_write", "slot_mapping", "sm_count", "table_width", "visible_window",
+    "PKV_ROPE_INTERLEAVED", "paged_attn_q4", "paged_attn_varlen", "paged_attn_window", "paged_kv_append",
+    "paged_kv_append_q4", "paged_kv_gather_q4", "paged_kv_write", "q4_block_bytes", "slot_mapping", "sm_count", "table_width", "visible_window",
     "workspace_size",
 )
 

@@ -23,15 +23,19 @@ PKV_CHECK_BOUNDS = 0x1
 PKV_FORCE_SIMT = 0x2
 PKV_NO_SPLIT = 0x4
 PKV_CONTIGUOUS_KV = 0x8
+PKV_ROPE_INTERLEAVED = 0x10
 PKV_SEG_CAUSAL, PKV_SEG_FULL = 0, 1
 PKV_DEVERR_SLOT, PKV_DEVERR_BLOCK, PKV_DEVERR_SEQLEN, PKV_DEVERR_QUERY, PKV_DEVERR_SEGMENT = 1, 2, 4, 8, 16
 PKV_DEVERR_TIMEOUT = 32
+PKV_DEVERR_POSITION = 64
 
 EXPORTS = (
     "pkv_last_error", "pkv_version", "build_segments", "pkv_slot_mapping", "pkv_table_width",
     "pkv_visible_window", "pkv_block_table_row", "paged_kv_write", "paged_attn_workspace_size",
     "paged_attn_varlen", "pkv_check", "pkv_sm_count", "pkv_last_launches", "paged_attn_varlen_noalloc",
     "paged_kv_gather", "paged_kv_write_attn", "pkv_selftest_wait", "pkv_last_split_plan",
+    "paged_kv_append", "pkv_q4_block_bytes", "paged_kv_append_q4", "paged_kv_gather_q4", "paged_attn_window",
+    "paged_attn_q4",
 )
 
 
@@ -87,7 +91,17 @@ def _load() -> C.CDLL:
         "paged_attn_varlen_noalloc": (C.c_int, [vp, C.c_int64, C.c_int, vp, vp, C.c_int64, C.c_int, C.c_int, C.c_int,
                                                 C.c_int, vp, C.c_int, C.c_int, vp, vp, C.c_int, C.c_int, C.c_float, vp,
                                                 vp, vp, C.c_uint32, vp]),
+        "pkv_q4_block_bytes": (C.c_size_t, [C.c_int]),
+        "paged_kv_gather_q4": (C.c_int, [vp, vp, C.c_int64, vp, C.c_int, C.c_int, C.c_int, C.c_int, vp, vp, C.c_int64,
+                                         C.c_int, C.c_int, C.c_int, C.c_uint32, vp]),
     }
+    for name in ("paged_kv_append", "paged_kv_append_q4"):
+        sig[name] = (C.c_int, [vp, C.c_int64, vp, C.c_int64, vp, C.c_int64, vp, vp, C.c_int64, C.c_int, vp, C.c_int64,
+                               C.c_int, vp, vp, vp, C.c_int64, C.c_int, C.c_int, C.c_int, C.c_uint32, vp])
+    for name in ("paged_attn_window", "paged_attn_q4"):
+        sig[name] = (C.c_int, [vp, C.c_int64, C.c_int, vp, vp, C.c_int64, C.c_int, C.c_int, C.c_int, C.c_int, vp,
+                               C.c_int, C.c_int, vp, vp, C.c_int, C.c_int, C.c_float, C.c_int, C.c_int, vp, C.c_uint32,
+                               vp])
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -375,6 +389,177 @@ def paged_attn_varlen_noalloc(q, key_pool, value_pool, block_table, query_start_
                                       int(max_query_len), int(max_seq_len), float(softmax_scale), _dptr(segs),
                                       _dptr(seg_start), _dptr(out), flags, _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- serving: rotary append, 4-bit pools, windows
+
+
+def q4_block_bytes(head_dim: int) -> int:
+    """Bytes of one (block, head) record of a 4-bit pool: pools are uint8 ``[num_blocks, Hkv, q4_block_bytes(D)]``."""
+    n = int(lib.pkv_q4_block_bytes(int(head_dim)))
+    if n == 0:
+        raise PkvError(PKV_ERR_UNSUPPORTED, f"4-bit pools hold heads of 64 or 128 channels (got {head_dim})")
+    return n
+
+
+def _token_stride(fn: str, name: str, x) -> int:
+    """Elements between the tokens of ``x [T, H, D]``, whose heads and channels must be contiguous."""
+    T, h, d = x.shape
+    st, sh, sd = x.stride()
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
+        raise ValueError(f"{fn}: {name}'s heads and channels must be contiguous (strides {tuple(x.stride())})")
+    if T <= 1:
+        return h * d
+    if st < 0:
+        raise ValueError(f"{fn}: {name} has a negative token stride")
+    return st
+
+
+def _append(fn: str, entry, q4: bool, q, k, v, positions, cos_sin, slot_mapping, key_pool, value_pool, interleaved,
+            q_out, flags, stream):
+    torch = _torch()
+    if k.dim() != 3 or v.shape != k.shape:
+        raise ValueError(f"{fn}: k and v must be [T, Hkv, D]")
+    T, hkv, d = k.shape
+    hq = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d:
+            raise ValueError(f"{fn}: q must be [T, Hq, D]")
+        hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, hq, d), dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape:
+            raise ValueError(f"{fn}: q_out shape {tuple(q_out.shape)} differs from q {tuple(q.shape)}")
+    elif q_out is not None:
+        raise ValueError(f"{fn}: q_out given without q")
+    if key_pool.shape != value_pool.shape or key_pool.dim() != 3:
+        raise ValueError(f"{fn}: the pools must be 3-D and of one shape")
+    if q4:
+        if key_pool.shape[1:] != (hkv, q4_block_bytes(d)):
+            raise ValueError(f"{fn}: the pools must be [num_blocks, {hkv}, {q4_block_bytes(d)}]")
+        if key_pool.dtype != torch.uint8 or value_pool.dtype != torch.uint8:
+            raise ValueError(f"{fn}: 4-bit pools are uint8")
+    elif key_pool.shape[1:] != (hkv, d):
+        raise ValueError(f"{fn}: the pools must be [num_slots, {hkv}, {d}]")
+    elif key_pool.dtype != k.dtype or value_pool.dtype != k.dtype:
+        raise ValueError(f"{fn}: sources and pools must share one dtype")
+    if v.dtype != k.dtype or (q is not None and (q.dtype != k.dtype or q_out.dtype != k.dtype)):
+        raise ValueError(f"{fn}: q, k, v and q_out must share one dtype")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
+        raise ValueError(f"{fn}: slot_mapping must be int64 [T]")
+    rot, max_position = 0, 0
+    if cos_sin is not None:
+        if positions is None or positions.dtype != torch.int32 or positions.numel() != T:
+            raise ValueError(f"{fn}: positions must be int32 [T]")
+        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
+            raise ValueError(f"{fn}: cos_sin must be float32 [max_position, rot_dim]")
+        max_position, rot = cos_sin.shape
+    _require(fn, slot_mapping, q_out, key_pool, value_pool, positions if rot else None, cos_sin if rot else None)
+    for x in (q, k, v):
+        if x is not None and x.device != key_pool.device:
+            raise ValueError(f"{fn}: tensors must be on one CUDA device (got {x.device})")
+    _ok(entry(_dptr(q), 0 if q is None else _token_stride(fn, "q", q), _dptr(k), _token_stride(fn, "k", k), _dptr(v),
+              _token_stride(fn, "v", v), _dptr(positions) if rot else 0, _dptr(cos_sin) if rot else 0, max_position,
+              rot, _dptr(slot_mapping), T, hq, _dptr(q_out), _dptr(key_pool), _dptr(value_pool), key_pool.shape[0],
+              hkv, d, dtype_code(k), flags | (PKV_ROPE_INTERLEAVED if interleaved else 0), _stream(stream)))
+    return q_out
+
+
+def paged_kv_append(q, k, v, positions, cos_sin, slot_mapping, key_pool, value_pool, *, interleaved: bool = False,
+                    q_out=None, flags: int = 0, stream=None):
+    """Rotate q and k by position, scatter k and v into the pools ``[num_slots, Hkv, D]``; returns ``q_out``.
+
+    q, k and v may be slices of one projection (any token stride); ``q=None`` appends only.  ``cos_sin`` is float32
+    ``[max_position, rot_dim]``, cosines then sines; ``None`` rotates nothing.  See include/pagedkv.h.
+    """
+    return _append("paged_kv_append", lib.paged_kv_append, False, q, k, v, positions, cos_sin, slot_mapping, key_pool,
+                   value_pool, interleaved, q_out, flags, stream)
+
+
+def paged_kv_append_q4(q, k, v, positions, cos_sin, slot_mapping, key_pool, value_pool, *, interleaved: bool = False,
+                       q_out=None, flags: int = 0, stream=None):
+    """paged_kv_append into 4-bit pools (uint8 ``[num_blocks, Hkv, q4_block_bytes(D)]``); returns ``q_out``."""
+    return _append("paged_kv_append_q4", lib.paged_kv_append_q4, True, q, k, v, positions, cos_sin, slot_mapping,
+                   key_pool, value_pool, interleaved, q_out, flags, stream)
+
+
+def paged_kv_gather_q4(key_pool, value_pool, block_table, stage_k, stage_v, *, first_block: int = 0,
+                       n_blocks: int | None = None, flags: int = 0, stream=None) -> None:
+    """The values of table blocks [first_block, first_block + n_blocks) of every row, into ``stage_k/v [B, rows, Hkv, D]``."""
+    fn, torch = "paged_kv_gather_q4", _torch()
+    if block_table.dim() != 2 or stage_k.dim() != 4 or key_pool.dim() != 3:
+        raise ValueError(f"{fn}: block_table must be [B, W], staging [B, rows, Hkv, D], pools [num_blocks, Hkv, bytes]")
+    B, W = block_table.shape
+    hkv, d = stage_k.shape[2:]
+    if n_blocks is None:
+        n_blocks = W - first_block
+    if stage_v.shape != stage_k.shape or stage_k.shape[0] != B or stage_v.dtype != stage_k.dtype:
+        raise ValueError(f"{fn}: staging buffers must be [B, rows, Hkv, D], of one dtype")
+    if key_pool.shape != value_pool.shape or key_pool.shape[1:] != (hkv, q4_block_bytes(d)):
+        raise ValueError(f"{fn}: the pools must be [num_blocks, {hkv}, {q4_block_bytes(d)}]")
+    if key_pool.dtype != torch.uint8 or value_pool.dtype != torch.uint8:
+        raise ValueError(f"{fn}: 4-bit pools are uint8")
+    _require(fn, key_pool, value_pool, block_table, stage_k, stage_v)
+    _require_metadata(fn, block_table)
+    _ok(lib.paged_kv_gather_q4(_dptr(key_pool), _dptr(value_pool), key_pool.shape[0], _dptr(block_table), B, W,
+                               int(first_block), int(n_blocks), _dptr(stage_k), _dptr(stage_v), stage_k.shape[1], hkv,
+                               d, dtype_code(stage_k), flags, _stream(stream)))
+
+
+def _attn_window(fn: str, entry, q4: bool, q, key_pool, value_pool, block_table, query_start_loc, seq_lens,
+                 max_query_len, max_seq_len, softmax_scale, window, sinks, out, flags, block_size, stream):
+    torch = _torch()
+    if q.dim() != 3 or key_pool.dim() != 3 or block_table.dim() != 2:
+        raise ValueError(f"{fn}: q must be [Tq, Hq, D], the pools 3-D and block_table [B, W]")
+    Tq, hq, d = q.shape
+    B, W = block_table.shape
+    hkv = key_pool.shape[1]
+    if value_pool.shape != key_pool.shape:
+        raise ValueError(f"{fn}: value_pool shape {tuple(value_pool.shape)} differs from key_pool {tuple(key_pool.shape)}")
+    if q4:
+        if key_pool.shape[2] != q4_block_bytes(d):
+            raise ValueError(f"{fn}: the pools must be [num_blocks, Hkv, {q4_block_bytes(d)}]")
+        num_blocks, pool_dtype = key_pool.shape[0], torch.uint8
+    else:
+        if key_pool.shape[2] != d or key_pool.shape[0] % block_size:
+            raise ValueError(f"{fn}: the pools must be [num_blocks * {block_size}, Hkv, {d}]")
+        num_blocks, pool_dtype = key_pool.shape[0] // block_size, q.dtype
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
+        raise ValueError(f"{fn}: out shape {tuple(out.shape)} differs from q {tuple(q.shape)}")
+    if query_start_loc.numel() != B + 1 or seq_lens.numel() != B:
+        raise ValueError(f"{fn}: query_start_loc must hold B+1 = {B + 1} and seq_lens B = {B} entries "
+                         f"(got {query_start_loc.numel()} and {seq_lens.numel()})")
+    _require(fn, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, out)
+    if key_pool.dtype != pool_dtype or value_pool.dtype != pool_dtype or out.dtype != q.dtype:
+        raise ValueError(f"{fn}: the pools must be {pool_dtype} and out of q's dtype")
+    _require_metadata(fn, block_table, query_start_loc, seq_lens)
+    _ok(entry(_dptr(q), Tq, hq, _dptr(key_pool), _dptr(value_pool), num_blocks, block_size, hkv, d, dtype_code(q),
+              _dptr(block_table), B, W, _dptr(query_start_loc), _dptr(seq_lens), int(max_query_len), int(max_seq_len),
+              float(softmax_scale), int(window), int(sinks), _dptr(out), flags, _stream(stream)))
+    return out
+
+
+def paged_attn_window(q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len: int,
+                      max_seq_len: int, softmax_scale: float, *, window: int = 0, sinks: int = 0, out=None,
+                      flags: int = 0, block_size: int = 16, stream=None):
+    """Causal paged attention: query p sees key j <= p when ``window == 0``, ``j < sinks`` or ``p - j < window``.
+
+    Pools are ``[num_blocks * 16, Hkv, D]`` of q's dtype; a row's queries are the last of its keys.  Returns ``out``.
+    """
+    return _attn_window("paged_attn_window", lib.paged_attn_window, False, q, key_pool, value_pool, block_table,
+                        query_start_loc, seq_lens, max_query_len, max_seq_len, softmax_scale, window, sinks, out,
+                        flags, block_size, stream)
+
+
+def paged_attn_q4(q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len: int,
+                  max_seq_len: int, softmax_scale: float, *, window: int = 0, sinks: int = 0, out=None,
+                  flags: int = 0, block_size: int = 16, stream=None):
+    """paged_attn_window over 4-bit pools (uint8 ``[num_blocks, Hkv, q4_block_bytes(D)]``); returns ``out``."""
+    return _attn_window("paged_attn_q4", lib.paged_attn_q4, True, q, key_pool, value_pool, block_table,
+                        query_start_loc, seq_lens, max_query_len, max_seq_len, softmax_scale, window, sinks, out,
+                        flags, block_size, stream)
 
 
 def check(stream=None) -> int:

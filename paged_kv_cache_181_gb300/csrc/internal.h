@@ -4,6 +4,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "pagedkv.h"
 
 // Record a failure message for pkv_last_error() and return `code`.
@@ -82,3 +84,55 @@ int pkv_launch_attn_combine(const PkvAttnArgs& a, pkv_dtype dt, void* stream);
 // tcgen05 path; returns -1 when the shape is not handled by it.
 int pkv_launch_attn_tc(const PkvAttnArgs& a, pkv_dtype dt, void* stream);
 bool pkv_attn_tc_supports(pkv_dtype dt, int D);
+
+// ---------------------------------------------------------------- serving operators
+
+// Rotary append into 16-bit/fp32 pools (rows of Hkv*D elements per slot) or 4-bit ones (records, q4.cuh).
+struct PkvAppendArgs {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  const int32_t* positions;
+  const float* cos_sin;  // [max_position, rot_dim]
+  int64_t max_position;
+  const int64_t* slots;
+  void *q_out, *k_pool, *v_pool;
+  int64_t num_slots, T;
+  int Hq, Hkv, D, rot_dim;
+  int interleaved, check;
+  unsigned int* err;
+};
+
+// Causal attention with a sliding window and sinks over a 16-bit/fp32 or 4-bit pool.
+struct PkvWinArgs {
+  const void* q;
+  const void* k_pool;
+  const void* v_pool;
+  void* out;
+  const int32_t* block_table;
+  const int32_t* query_start_loc;
+  const int32_t* seq_lens;
+  unsigned int* err;
+  int64_t num_blocks;
+  int B, W, Hq, Hkv;
+  int max_query_len, max_seq_len;
+  int window, sinks;
+  int check;
+  float scale;
+};
+
+// Launchers (each returns a cudaError_t as an int, 0 == success).
+int pkv_launch_append(const PkvAppendArgs& a, pkv_dtype dt, bool q4, void* stream);
+int pkv_launch_gather_q4(const void* kp, const void* vp, int64_t num_blocks, const int32_t* table, int B, int W,
+                         int first_block, int n_blocks, void* sk, void* sv, int64_t stage_rows, int Hkv, int D,
+                         pkv_dtype dt, unsigned int* err, int check, void* stream);
+int pkv_launch_win_simt(const PkvWinArgs& a, pkv_dtype dt, int D, bool q4, void* stream);
+
+// Shared by those launchers (serving.cu).
+// Per-context, once per kernel: opt in to `smem` bytes of dynamic shared memory and to clusters of 16.
+int pkv_prepare_kernel(const void* kernel, int smem, std::atomic<uint64_t> (&done)[64]);
+// Keys that a tile of `tokens` query tokens can see, from the sizes the host knows.
+int64_t pkv_visible_keys(const PkvWinArgs& a, int64_t tokens);
+// CTAs (1, 2, 4, 8 or 16) that share one item's `steps` key steps, `per_sm` CTAs being resident on an SM.
+int pkv_plan_cluster(int64_t items, int64_t steps, int per_sm);
+int pkv_launch_cluster(const void* kernel, int64_t items, int ctas, int threads, size_t smem, const PkvWinArgs* a,
+                       void* stream);

@@ -1,0 +1,252 @@
+// Entry points of the serving operators: rotary append, 4-bit pools, window/sinks attention.  Argument checks,
+// the choice of kernel, and the plan of how many CTAs share an item's keys.
+
+#include <math.h>
+
+#include "common.cuh"
+
+namespace {
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+constexpr int64_t kMaxGrid = 0x7fffffff;
+
+pkv_status check_dtype(const char* fn, pkv_dtype dt) {
+  if (dt == PKV_F32 || dt == PKV_BF16 || dt == PKV_F16) return PKV_OK;
+  return pkv_fail(PKV_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, (int)dt);
+}
+
+pkv_status append_impl(const char* fn, bool q4, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                       const void* v, int64_t v_stride, const int32_t* positions, const float* cos_sin,
+                       int64_t max_position, int rot_dim, const int64_t* slots, int64_t T, int Hq, void* q_out,
+                       void* key_pool, void* value_pool, int64_t num_slots, int Hkv, int D, pkv_dtype dt,
+                       uint32_t flags, void* stream) {
+  pkv_clear_error();
+  pkv_set_launches(0);
+  if (T < 0 || num_slots < 0 || max_position < 0 || Hq < 0 || Hkv <= 0)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: negative or zero size (T=%lld, Hq=%d, Hkv=%d)", fn, (long long)T, Hq, Hkv);
+  if (D != 64 && D != 128) return pkv_fail(PKV_ERR_UNSUPPORTED, "%s: head dim must be 64 or 128 (got %d)", fn, D);
+  if (pkv_status st = check_dtype(fn, dt)) return st;
+  if (rot_dim < 0 || rot_dim > D)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: rot_dim must be in [0, %d] (got %d)", fn, D, rot_dim);
+  if (rot_dim % 16) return pkv_fail(PKV_ERR_UNSUPPORTED, "%s: rot_dim must be a multiple of 16 (got %d)", fn, rot_dim);
+  if (T > kMaxGrid || (int64_t)Hq + 2 * (int64_t)Hkv > 65535)
+    return pkv_fail(PKV_ERR_UNSUPPORTED, "%s: too many tokens or heads for one call (T=%lld, Hq=%d, Hkv=%d)", fn,
+                    (long long)T, Hq, Hkv);
+  if (T == 0) return PKV_OK;
+  if ((Hq > 0 && (!q || !q_out)) || !k || !v || !slots || !key_pool || !value_pool ||
+      (rot_dim && (!positions || !cos_sin)))
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+  const int size = pkv_dtype_size(dt);
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(key_pool) ||
+      !aligned16(value_pool) || !aligned16(rot_dim ? cos_sin : nullptr) || (Hq && (q_stride * size) % 16) ||
+      (k_stride * size) % 16 || (v_stride * size) % 16)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: base pointers and token strides must be 16-byte aligned", fn);
+  if (Hq && q == q_out && T > 1 && q_stride != (int64_t)Hq * D)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: q_out may be q only when q is contiguous", fn);
+  PkvAppendArgs a{};
+  a.q = q, a.k = k, a.v = v;
+  a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+  a.positions = positions, a.cos_sin = cos_sin, a.max_position = max_position;
+  a.slots = slots, a.q_out = q_out, a.k_pool = key_pool, a.v_pool = value_pool;
+  a.num_slots = num_slots, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.D = D, a.rot_dim = rot_dim;
+  a.interleaved = (flags & PKV_ROPE_INTERLEAVED) ? 1 : 0;
+  a.check = (flags & PKV_CHECK_BOUNDS) ? 1 : 0;
+  a.err = a.check ? pkv_device_error_word() : nullptr;
+  if (a.check && !a.err) return pkv_fail(PKV_ERR_CUDA, "%s: device error word unavailable", fn);
+  const int rc = pkv_launch_append(a, dt, q4, stream);
+  if (rc) return pkv_fail(PKV_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString((cudaError_t)rc));
+  pkv_set_launches(1);
+  return PKV_OK;
+}
+
+pkv_status win_impl(const char* fn, bool q4, const void* q, int64_t Tq, int Hq, const void* key_pool,
+                    const void* value_pool, int64_t num_blocks, int block_size, int Hkv, int D, pkv_dtype dt,
+                    const int32_t* block_table, int B, int W, const int32_t* query_start_loc, const int32_t* seq_lens,
+                    int max_query_len, int max_seq_len, float softmax_scale, int window, int sinks, void* out,
+                    uint32_t flags, void* stream) {
+  pkv_clear_error();
+  pkv_set_launches(0);
+  if (Tq < 0 || B < 0 || W < 0 || max_query_len < 0 || max_seq_len < 0 || num_blocks < 0)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv)
+    return pkv_fail(PKV_ERR_INVALID_ARG,
+                    "%s: num_heads must be a positive multiple of num_kv_heads (Hq=%d, Hkv=%d)", fn, Hq, Hkv);
+  if (block_size != 16) return pkv_fail(PKV_ERR_UNSUPPORTED, "%s: block_size must be 16 (got %d)", fn, block_size);
+  if (D != 64 && D != 128) return pkv_fail(PKV_ERR_UNSUPPORTED, "%s: head dim must be 64 or 128 (got %d)", fn, D);
+  if (pkv_status st = check_dtype(fn, dt)) return st;
+  if (window < 0 || sinks < 0)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: window and sinks must not be negative (%d, %d)", fn, window, sinks);
+  if (!isfinite(softmax_scale)) return pkv_fail(PKV_ERR_INVALID_ARG, "%s: softmax_scale is not finite", fn);
+  if (dt != PKV_F32 && !(softmax_scale > 0.f) && !(flags & PKV_FORCE_SIMT))
+    return pkv_fail(PKV_ERR_UNSUPPORTED,
+                    "%s: a bf16/f16 call needs softmax_scale > 0 (got %g); pass PKV_FORCE_SIMT to run it on the "
+                    "CUDA-core kernel", fn, (double)softmax_scale);
+  if ((int64_t)max_seq_len > (int64_t)W * block_size)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: max_seq_len %d exceeds the table's %d x %d slots", fn, max_seq_len, W,
+                    block_size);
+  if (Tq > kMaxGrid || (int64_t)max_query_len * (Hq / Hkv) > kMaxGrid - 1024)
+    return pkv_fail(PKV_ERR_UNSUPPORTED, "%s: too many queries for one call", fn);
+  if (Tq == 0 || B == 0 || max_query_len == 0) return PKV_OK;
+  if (!q || !key_pool || !value_pool || !block_table || !query_start_loc || !seq_lens || !out)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+  if (!aligned16(q) || !aligned16(key_pool) || !aligned16(value_pool) || !aligned16(out))
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: q, pools and out must be 16-byte aligned", fn);
+  if (num_blocks == 0 && max_seq_len > 0)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: keys of up to %d positions in a pool without blocks", fn, max_seq_len);
+  PkvWinArgs a{};
+  a.q = q, a.k_pool = key_pool, a.v_pool = value_pool, a.out = out;
+  a.block_table = block_table, a.query_start_loc = query_start_loc, a.seq_lens = seq_lens;
+  a.num_blocks = num_blocks, a.B = B, a.W = W, a.Hq = Hq, a.Hkv = Hkv;
+  a.max_query_len = max_query_len, a.max_seq_len = max_seq_len, a.window = window, a.sinks = sinks;
+  a.check = (flags & PKV_CHECK_BOUNDS) ? 1 : 0;
+  a.scale = softmax_scale;
+  a.err = pkv_device_error_word();
+  if (!a.err) return pkv_fail(PKV_ERR_CUDA, "%s: device error word unavailable", fn);
+  const int rc = pkv_launch_win_simt(a, dt, D, q4, stream);
+  if (rc) return pkv_fail(PKV_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString((cudaError_t)rc));
+  pkv_set_launches(1);
+  return PKV_OK;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- launches
+
+int pkv_prepare_kernel(const void* kernel, int smem, std::atomic<uint64_t> (&done)[64]) {
+  // Keyed on the context: function attributes belong to the context they were set in.
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool cached = dev >= 0 && dev < 64;
+  const uint64_t ctx = pkv_context_id();
+  if (cached && ctx != 0 && done[dev].load(std::memory_order_acquire) == ctx) return 0;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && cached) done[dev].store(ctx, std::memory_order_release);
+  return (int)e;
+}
+
+int64_t pkv_visible_keys(const PkvWinArgs& a, int64_t tokens) {
+  int64_t keys = a.max_seq_len;
+  if (a.window > 0) {
+    const int64_t most = (int64_t)a.window + tokens + a.sinks + 32;
+    if (most < keys) keys = most;
+  }
+  return keys;
+}
+
+// A launch runs its items' CTAs in waves of (SMs x per_sm); a CTA takes its share of the steps plus a fixed cost
+// (set-up, merge) of about four steps.  The smallest estimate wins; the more CTAs only where they gain a tenth.
+int pkv_plan_cluster(int64_t items, int64_t steps, int per_sm) {
+  int sms = pkv_sm_count();
+  if (sms <= 0) sms = 152;
+  const int64_t slots = (int64_t)sms * per_sm;
+  int best = 1;
+  double best_cost = 1e300;
+  for (int c = 1; c <= 16; c *= 2) {
+    if (c > 1 && (steps < 2 * c || items * c > kMaxGrid)) break;
+    const double waves = (double)((items * c + slots - 1) / slots);
+    const double cost = waves * ((double)((steps + c - 1) / c) + 4.0);
+    if (cost < 0.9 * best_cost) best = c, best_cost = cost;
+  }
+  return best;
+}
+
+int pkv_launch_cluster(const void* kernel, int64_t items, int ctas, int threads, size_t smem, const PkvWinArgs* a,
+                       void* stream) {
+  if (items * ctas > kMaxGrid) return (int)cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * ctas));
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {const_cast<PkvWinArgs*>(a)};
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
+  const cudaError_t last = cudaGetLastError();
+  return (int)(e != cudaSuccess ? e : last);
+}
+
+// ---------------------------------------------------------------- C entries
+
+extern "C" size_t pkv_q4_block_bytes(int D) { return D == 64 || D == 128 ? (size_t)10 * D : 0; }
+
+extern "C" pkv_status paged_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                      int64_t v_stride, const int32_t* positions, const float* cos_sin,
+                                      int64_t max_position, int rot_dim, const int64_t* slot_mapping, int64_t T,
+                                      int Hq, void* q_out, void* key_pool, void* value_pool, int64_t num_slots,
+                                      int Hkv, int D, pkv_dtype dt, uint32_t flags, void* stream) {
+  return append_impl("paged_kv_append", false, q, q_stride, k, k_stride, v, v_stride, positions, cos_sin, max_position,
+                     rot_dim, slot_mapping, T, Hq, q_out, key_pool, value_pool, num_slots, Hkv, D, dt, flags, stream);
+}
+
+extern "C" pkv_status paged_kv_append_q4(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                         const void* v, int64_t v_stride, const int32_t* positions,
+                                         const float* cos_sin, int64_t max_position, int rot_dim,
+                                         const int64_t* slot_mapping, int64_t T, int Hq, void* q_out, void* key_pool,
+                                         void* value_pool, int64_t num_blocks, int Hkv, int D, pkv_dtype dt,
+                                         uint32_t flags, void* stream) {
+  if (num_blocks > INT64_MAX / 16) num_blocks = INT64_MAX / 16;
+  return append_impl("paged_kv_append_q4", true, q, q_stride, k, k_stride, v, v_stride, positions, cos_sin,
+                     max_position, rot_dim, slot_mapping, T, Hq, q_out, key_pool, value_pool, num_blocks * 16, Hkv, D,
+                     dt, flags, stream);
+}
+
+extern "C" pkv_status paged_kv_gather_q4(const void* key_pool, const void* value_pool, int64_t num_blocks,
+                                         const int32_t* block_table, int B, int W, int first_block, int n_blocks,
+                                         void* stage_k, void* stage_v, int64_t stage_rows, int Hkv, int D,
+                                         pkv_dtype dt, uint32_t flags, void* stream) {
+  const char* fn = "paged_kv_gather_q4";
+  pkv_clear_error();
+  pkv_set_launches(0);
+  if (B < 0 || W < 0 || first_block < 0 || n_blocks < 0 || num_blocks < 0 || stage_rows < 0 || Hkv <= 0)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: negative or zero size", fn);
+  if (D != 64 && D != 128) return pkv_fail(PKV_ERR_UNSUPPORTED, "%s: head dim must be 64 or 128 (got %d)", fn, D);
+  if (pkv_status st = check_dtype(fn, dt)) return st;
+  if ((int64_t)first_block + n_blocks > W)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: blocks [%d, %d) run past the table width %d", fn, first_block,
+                    first_block + n_blocks, W);
+  if (((int64_t)first_block + n_blocks) * 16 > stage_rows)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: %d blocks do not fit %lld staging rows", fn, first_block + n_blocks,
+                    (long long)stage_rows);
+  if (B == 0 || n_blocks == 0) return PKV_OK;
+  if (!key_pool || !value_pool || !block_table || !stage_k || !stage_v)
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+  if (!aligned16(key_pool) || !aligned16(value_pool) || !aligned16(stage_k) || !aligned16(stage_v))
+    return pkv_fail(PKV_ERR_INVALID_ARG, "%s: base pointers must be 16-byte aligned", fn);
+  const int check = (flags & PKV_CHECK_BOUNDS) ? 1 : 0;
+  unsigned int* err = check ? pkv_device_error_word() : nullptr;
+  if (check && !err) return pkv_fail(PKV_ERR_CUDA, "%s: device error word unavailable", fn);
+  const int rc = pkv_launch_gather_q4(key_pool, value_pool, num_blocks, block_table, B, W, first_block, n_blocks,
+                                      stage_k, stage_v, stage_rows, Hkv, D, dt, err, check, stream);
+  if (rc) return pkv_fail(PKV_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString((cudaError_t)rc));
+  pkv_set_launches(1);
+  return PKV_OK;
+}
+
+extern "C" pkv_status paged_attn_window(const void* q, int64_t Tq, int Hq, const void* key_pool,
+                                        const void* value_pool, int64_t num_blocks, int block_size, int Hkv, int D,
+                                        pkv_dtype dt, const int32_t* block_table, int B, int W,
+                                        const int32_t* query_start_loc, const int32_t* seq_lens, int max_query_len,
+                                        int max_seq_len, float softmax_scale, int window, int sinks, void* out,
+                                        uint32_t flags, void* stream) {
+  return win_impl("paged_attn_window", false, q, Tq, Hq, key_pool, value_pool, num_blocks, block_size, Hkv, D, dt,
+                  block_table, B, W, query_start_loc, seq_lens, max_query_len, max_seq_len, softmax_scale, window,
+                  sinks, out, flags, stream);
+}
+
+extern "C" pkv_status paged_attn_q4(const void* q, int64_t Tq, int Hq, const void* key_pool, const void* value_pool,
+                                    int64_t num_blocks, int block_size, int Hkv, int D, pkv_dtype dt,
+                                    const int32_t* block_table, int B, int W, const int32_t* query_start_loc,
+                                    const int32_t* seq_lens, int max_query_len, int max_seq_len, float softmax_scale,
+                                    int window, int sinks, void* out, uint32_t flags, void* stream) {
+  return win_impl("paged_attn_q4", true, q, Tq, Hq, key_pool, value_pool, num_blocks, block_size, Hkv, D, dt,
+                  block_table, B, W, query_start_loc, seq_lens, max_query_len, max_seq_len, softmax_scale, window,
+                  sinks, out, flags, stream);
+}

@@ -1,0 +1,415 @@
+"""GPU: rotary append, 4-bit pools and window/sinks attention against their 64-bit definitions."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving as sv
+
+from . import serving_cases as sc
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from paged_kv_cache_181_gb300 import _lib
+
+    return _lib
+
+
+# ---------------------------------------------------------------- append
+
+
+def append_inputs(T, hq, hkv, d, dtype, rot, seed, fused, blocks, skip=()):
+    g = torch.Generator().manual_seed(seed)
+    qkv = torch.randn(T, hq + 2 * hkv, d, generator=g).to(sc.DT[dtype])
+    if fused:
+        dev = qkv.cuda()
+        q, k, v = dev[:, :hq], dev[:, hq:hq + hkv], dev[:, hq + hkv:]
+    else:
+        q, k, v = (x.contiguous().cuda() for x in (qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]))
+    angle = torch.rand(50, max(rot // 2, 1), generator=g) * 300
+    cs = torch.cat([angle.cos(), angle.sin()], 1) if rot else None
+    pos = torch.randint(0, 50, (T,), generator=g, dtype=torch.int32)
+    slots = torch.randperm(blocks * 16, generator=g)[:T].to(torch.int64)
+    for t in skip:
+        slots[t] = -1
+    return qkv, q, k, v, pos, cs, slots
+
+
+def bits(t):
+    t = t.contiguous().cpu()
+    return t.view({4: torch.int32, 2: torch.int16, 1: torch.uint8}[t.element_size()]).numpy()
+
+
+def rotated(x, pos, cs, interleaved):
+    """Bit-exact fp32 rotation, then one rounding to x's type."""
+    if cs is None:
+        return x, x.float().numpy()
+    y = sv.rotate(x.float().numpy(), pos.numpy(), cs.numpy(), interleaved, np.float32)
+    return torch.from_numpy(y).to(x.dtype), y
+
+
+APPEND = [
+    # T, hq, hkv, d, rot, interleaved, fused
+    (1, 32, 8, 128, 128, False, True),
+    (1, 1, 1, 64, 64, False, False),
+    (5, 6, 2, 64, 32, True, True),
+    (33, 7, 1, 128, 64, False, True),
+    (17, 40, 8, 128, 128, True, False),
+    (257, 3, 3, 64, 16, False, True),
+    (19, 5, 5, 128, 112, False, False),
+    (9, 4, 2, 128, 48, True, True),
+    (40, 8, 2, 128, 0, False, True),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,hq,hkv,d,rot,inter,fused", APPEND)
+def test_append_bit_exact(lib, T, hq, hkv, d, rot, inter, fused, dtype):
+    blocks, skip = T // 16 + 3, ((1, 3) if T > 4 else ())
+    qkv, q, k, v, pos, cs, slots = append_inputs(T, hq, hkv, d, dtype, rot, T + d, fused, blocks, skip)
+    kp = torch.full((blocks * 16, hkv, d), 3.0, dtype=sc.DT[dtype], device="cuda")
+    vp = torch.full_like(kp, -5.0)
+    want_k, want_v = kp.cpu(), vp.cpu()
+    out = lib.paged_kv_append(q, k, v, pos.cuda(), None if cs is None else cs.cuda(), slots.cuda(), kp, vp,
+                              interleaved=inter, flags=lib.PKV_CHECK_BOUNDS)
+    assert lib.check() == 0 and lib.last_launches() == 1
+    keep = slots >= 0
+    want_k[slots[keep]] = rotated(qkv[:, hq:hq + hkv], pos, cs, inter)[0][keep]
+    want_v[slots[keep]] = qkv[:, hq + hkv:][keep]
+    assert np.array_equal(bits(out), bits(rotated(qkv[:, :hq], pos, cs, inter)[0]))
+    assert np.array_equal(bits(kp), bits(want_k)) and np.array_equal(bits(vp), bits(want_v))
+    if cs is not None and dtype == "f32":  # and near the 64-bit rotation: two products and a sum, rounded each
+        w = sv.rotate(qkv[:, :hq].double().numpy(), pos.numpy(), cs.double().numpy(), inter)
+        size = sv.rotate(qkv[:, :hq].abs().double().numpy(), pos.numpy(),
+                         np.concatenate([cs[:, : rot // 2].abs(), -cs[:, rot // 2:].abs()], 1), inter)
+        other = sv.rotate(qkv[:, :hq].abs().double().numpy(), pos.numpy(), cs.abs().double().numpy(), inter)
+        assert (np.abs(out.double().cpu().numpy() - w) <= 2 * 2.0 ** -24 * np.maximum(size, other) + 1e-38).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,hq,hkv,d,rot,inter,fused", APPEND)
+def test_append_q4_and_gather_bit_exact(lib, T, hq, hkv, d, rot, inter, fused, dtype):
+    blocks, skip = T // 16 + 3, ((0, 2) if T > 4 else ())
+    qkv, q, k, v, pos, cs, slots = append_inputs(T, hq, hkv, d, dtype, rot, 3 * T + d, fused, blocks, skip)
+    pools = [sc.random_q4_pool(blocks, hkv, d, s) for s in (1, 2)]
+    kp, vp = (torch.from_numpy(p.copy()).cuda() for p in pools)
+    out = lib.paged_kv_append_q4(q, k, v, pos.cuda(), None if cs is None else cs.cuda(), slots.cuda(), kp, vp,
+                                 interleaved=inter, flags=lib.PKV_CHECK_BOUNDS)
+    assert lib.check() == 0 and lib.last_launches() == 1
+    sv.q4_store(pools[0], slots.tolist(), rotated(qkv[:, hq:hq + hkv], pos, cs, inter)[1])
+    sv.q4_store(pools[1], slots.tolist(), qkv[:, hq + hkv:].float().numpy())
+    assert np.array_equal(bits(out), bits(rotated(qkv[:, :hq], pos, cs, inter)[0]))
+    assert np.array_equal(kp.cpu().numpy(), pools[0]) and np.array_equal(vp.cpu().numpy(), pools[1])
+    # Read two rows' blocks back, from the second listed block on.
+    table = torch.randint(0, blocks, (2, 3), dtype=torch.int32, generator=torch.Generator().manual_seed(T))
+    stage = [torch.full((2, 50, hkv, d), 9.0, dtype=sc.DT[dtype], device="cuda") for _ in range(2)]
+    lib.paged_kv_gather_q4(kp, vp, table.cuda(), *stage, first_block=1, n_blocks=2, flags=lib.PKV_CHECK_BOUNDS)
+    assert lib.check() == 0
+    for pool, got in zip(pools, stage):
+        want = torch.full((2, 50, hkv, d), 9.0, dtype=sc.DT[dtype])
+        values = torch.from_numpy(sv.q4_load(pool)).view(blocks, 16, hkv, d)
+        want[:, 16:48] = values[table[:, 1:].long()].reshape(2, 32, hkv, d).to(sc.DT[dtype])
+        assert np.array_equal(bits(got), bits(want))
+
+
+def test_append_q4_odd_values(lib):
+    """Groups that are constant, huge, tiny, non-finite: stored as the format says."""
+    T, hkv, d = 6, 1, 64
+    x = np.random.default_rng(5).standard_normal((T, hkv, d)).astype(np.float32)
+    x[0, 0, :32] = 2.5
+    x[1, 0, 5] = 1e30
+    x[2, 0, 40] = np.inf
+    x[3, 0, 2] = np.nan
+    x[4] *= 1e-7
+    x[5, 0, :32] = 0
+    pool = np.zeros((1, hkv, 640), np.uint8)
+    v = torch.from_numpy(x).cuda()
+    slots = torch.arange(T, device="cuda")
+    kp, vp = torch.from_numpy(pool.copy()).cuda(), torch.from_numpy(pool.copy()).cuda()
+    assert lib.paged_kv_append_q4(None, v, v, None, None, slots, kp, vp) is None
+    sv.q4_store(pool, range(T), x)
+    want, got = sv.q4_load(pool), sv.q4_load(vp.cpu().numpy())
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got[~np.isnan(got)], want[~np.isnan(want)])
+    assert torch.equal(kp, vp)
+
+
+def test_append_in_place_and_on_another_stream(lib):
+    qkv, q, k, v, pos, cs, slots = append_inputs(37, 8, 2, 128, "bf16", 128, 3, False, 4)
+    kp, vp = (torch.zeros(64, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    want = lib.paged_kv_append(q, k, v, pos.cuda(), cs.cuda(), slots.cuda(), kp, vp).clone()
+    wk = kp.clone()
+    kp.zero_()
+    pos, cs, slots = pos.cuda(), cs.cuda(), slots.cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = lib.paged_kv_append(q, k, v, pos, cs, slots, kp, vp, q_out=q, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert got is q and torch.equal(q, want) and torch.equal(kp, wk)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_append_flags_bad_metadata(lib, q4):
+    qkv, q, k, v, pos, cs, slots = append_inputs(4, 2, 1, 64, "f16", 64, 8, False, 2)
+    pos[1], pos[2] = 50, -1
+    slots = torch.tensor([3, 4, 5, 32])
+    shape = (2, 1, 640) if q4 else (32, 1, 64)
+    kp, vp = (torch.zeros(shape, dtype=torch.uint8 if q4 else torch.float16, device="cuda") for _ in range(2))
+    out = torch.full((4, 2, 64), 7.0, dtype=torch.float16, device="cuda")
+    fn = lib.paged_kv_append_q4 if q4 else lib.paged_kv_append
+    fn(q, k, v, pos.cuda(), cs.cuda(), slots.cuda(), kp, vp, q_out=out, flags=lib.PKV_CHECK_BOUNDS)
+    assert lib.check() == lib.PKV_DEVERR_SLOT | lib.PKV_DEVERR_POSITION
+    assert (out[1:3] == 7).all() and not (out[0] == 7).any() and not (out[3] == 7).any()
+    held = sv.q4_load(vp.cpu().numpy())[:, 0] if q4 else vp[:, 0].float().cpu().numpy()
+    assert held[3].any() and not np.delete(held, 3, 0).any()
+
+
+def test_gather_q4_flags_bad_blocks(lib):
+    pool = torch.from_numpy(sc.random_q4_pool(2, 1, 64, 1)).cuda()
+    table = torch.tensor([[1, 2, -1, 0]], dtype=torch.int32).cuda()
+    stage = [torch.full((1, 64, 1, 64), 9.0, device="cuda") for _ in range(2)]
+    lib.paged_kv_gather_q4(pool, pool, table, *stage, flags=lib.PKV_CHECK_BOUNDS)
+    assert lib.check() == lib.PKV_DEVERR_BLOCK
+    assert (stage[0][0, 16:48] == 9).all() and not (stage[1][0, :16] == 9).any() and not (stage[0][0, 48:] == 9).any()
+
+
+# ---------------------------------------------------------------- attention
+
+
+def attention(lib, rows, hq, hkv, d, dtype, window, sinks, q4=False, seed=0, flags=0, scale=None, poison=True, tail=0,
+              table_pad=0):
+    """Run one call; returns (got, want, tolerance).  What no query sees is NaN, its blocks are not listed."""
+    g = torch.Generator().manual_seed(seed)
+    lens = [r[1] for r in rows]
+    table, blocks = sc.table_of(seed, lens, max(-(-max(lens) // 16), 1) + table_pad)
+    scale = d ** -0.5 if scale is None else scale
+    qsl = np.concatenate([[0], np.cumsum([r[0] for r in rows])]).astype(np.int32)
+    q = torch.randn(int(qsl[-1]) + tail, hq, d, generator=g).to(sc.DT[dtype])
+    if q4:
+        kn, vn = (sc.random_q4_pool(blocks, hkv, d, seed + s) for s in (1, 2))
+        k64, v64 = sv.q4_load(kn), sv.q4_load(vn)
+        kp, vp = torch.from_numpy(kn), torch.from_numpy(vn)
+    else:
+        kp, vp = (torch.randn(blocks * 16, hkv, d, generator=g).to(sc.DT[dtype]) for _ in range(2))
+        k64, v64 = kp.double().numpy(), vp.double().numpy()
+    want, spread, reach = sv.window_attention(q[: qsl[-1]].double().numpy(), k64, v64, table, qsl, lens, scale, window,
+                                              sinks)
+    if poison:
+        nan_pair = torch.tensor([float("nan")], dtype=torch.float16).view(torch.uint8)
+        kept = torch.zeros(blocks * 16, dtype=torch.bool)
+        for b, (sq, length) in enumerate(rows):
+            seen = sorted({j for i in range(sq) for j in sv.visible(length - sq + i, length, window, sinks)})
+            at = np.asarray(seen, dtype=np.int64)
+            if at.size:
+                kept[torch.from_numpy(table[b][at // 16].astype(np.int64) * 16 + at % 16)] = True
+        for b in range(len(rows)):
+            seen = sc.seen_blocks(rows, b, window, sinks)
+            for w in range(table.shape[1]):
+                if w not in seen:
+                    table[b, w] = -7 if w % 2 else 10 ** 6
+        for pool in (kp, vp):
+            if q4:  # NaN pairs for the unseen tokens
+                pairs = pool[:, :, 8 * d:].view(blocks, hkv, 16, d // 32, 2, 2).transpose(1, 2).reshape(blocks * 16, -1, 2)
+                pairs[~kept] = nan_pair
+                pool[:, :, 8 * d:] = pairs.view(blocks, 16, hkv, d // 8).transpose(1, 2).reshape(blocks, hkv, 2 * d)
+            else:
+                pool[~kept] = float("nan")
+    out = torch.full((q.shape[0], hq, d), 77.0, dtype=sc.DT[dtype], device="cuda")
+    fn = lib.paged_attn_q4 if q4 else lib.paged_attn_window
+    fn(q.cuda(), kp.cuda(), vp.cuda(), torch.from_numpy(table).cuda(), torch.from_numpy(qsl).cuda(),
+       torch.tensor(lens, dtype=torch.int32).cuda(), max(1, max(r[0] for r in rows)), max(lens), scale, window=window,
+       sinks=sinks, out=out, flags=flags | lib.PKV_CHECK_BOUNDS)
+    assert lib.check() == 0 and lib.last_launches() == 1
+    out = out.double().cpu().numpy()
+    assert (out[qsl[-1]:] == 77).all()
+    half = {"f32": 0.0, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dtype]
+    if q4 and dtype == "bf16":
+        half = 2.0 ** -11  # probabilities meet fp16 values
+    tol = sc.tolerance(want, spread, reach, max(lens), d, dtype, 0.0 if flags & lib.PKV_FORCE_SIMT else half)
+    return out[: qsl[-1]], want, tol
+
+
+def agree(got, want, tol):
+    off = np.abs(got - want)
+    assert not np.isnan(got).any()
+    assert (off <= tol).all(), (float(off.max()), float((off / tol).max()), np.unravel_index(np.argmax(off / tol), off.shape))
+
+
+ROWS = {
+    "tokens": [(1, 1), (1, 17), (1, 0), (1, 16), (1, 333), (1, 100), (1, 700)],
+    "few": [(2, 40), (0, 9), (5, 3), (3, 0), (4, 260), (8, 8), (3, 515)],
+    "chunks": [(40, 90), (1, 5), (17, 300), (130, 130)],
+    "long": [(1, 2600), (2, 1500)],
+}
+MASKS = [(0, 0), (1, 0), (7, 3), (64, 4), (100, 20), (33, 700)]
+PATHS = [("f32", False, 0), ("bf16", False, 0), ("f16", False, 0), ("bf16", True, 0), ("f16", True, 0), ("f32", True, 0),
+         ("bf16", False, 2), ("f16", True, 2)]
+
+
+@pytest.mark.parametrize("dtype,q4,flags", PATHS, ids=lambda v: str(v))
+@pytest.mark.parametrize("window,sinks", MASKS)
+@pytest.mark.parametrize("rows", list(ROWS))
+def test_attention_masks_and_lengths(lib, rows, window, sinks, dtype, q4, flags):
+    d = 128 if (window + len(rows)) % 2 else 64
+    agree(*attention(lib, ROWS[rows], 6, 2, d, dtype, window, sinks, q4, seed=window + 7, flags=flags))
+
+
+@pytest.mark.parametrize("q4,dtype", [(False, "bf16"), (False, "f32"), (True, "bf16"), (True, "f16")])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (5, 1), (8, 8), (16, 2), (40, 8), (33, 3), (64, 1), (12, 4)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_head_layouts(lib, hq, hkv, d, q4, dtype):
+    agree(*attention(lib, [(1, 129), (3, 70), (20, 64)], hq, hkv, d, dtype, 50, 5, q4, seed=hq + d))
+
+
+@pytest.mark.parametrize("q4,dtype", [(False, "bf16"), (False, "f16"), (False, "f32"), (True, "bf16")])
+@pytest.mark.parametrize("scale", [1.0, 0.01])
+def test_attention_scales_and_padded_batch(lib, q4, dtype, scale):
+    agree(*attention(lib, [(1, 300), (70, 200)], 4, 2, 128, dtype, 90, 2, q4, seed=5, scale=scale, tail=9, table_pad=3))
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_attention_negative_scale_by_name(lib, q4):
+    agree(*attention(lib, [(3, 50)], 4, 2, 64, "bf16", 20, 2, q4, seed=6, scale=-0.2, flags=lib.PKV_FORCE_SIMT))
+    agree(*attention(lib, [(3, 50)], 4, 2, 64, "f32", 20, 2, q4, seed=6, scale=-0.2))
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_attention_flags_bad_metadata(lib, q4):
+    hq, hkv, d = 4, 2, 64
+    pool = (torch.from_numpy(sc.random_q4_pool(8, hkv, d, 1)) if q4 else torch.randn(128, hkv, d).bfloat16()).cuda()
+    q = torch.randn(5, hq, d).bfloat16().cuda()
+    fn = lib.paged_attn_q4 if q4 else lib.paged_attn_window
+
+    def call(table, qsl, lens, mq=4, ml=64):
+        fn(q, pool, pool, torch.tensor(table, dtype=torch.int32).cuda(), torch.tensor(qsl, dtype=torch.int32).cuda(),
+           torch.tensor(lens, dtype=torch.int32).cuda(), mq, ml, 0.1, window=20, sinks=2, flags=lib.PKV_CHECK_BOUNDS)
+        return lib.check()
+
+    good = [[0, 1, 2, 3], [4, 5, 6, 7]]
+    assert call(good, [0, 2, 5], [64, 40]) == 0
+    assert call([[0, 1, 9, 3], [4, 5, 6, 7]], [0, 2, 5], [64, 40]) == lib.PKV_DEVERR_BLOCK
+    assert call(good, [0, 2, 5], [65, 40]) == lib.PKV_DEVERR_SEQLEN
+    assert call(good, [0, 2, 5], [64, -3]) == lib.PKV_DEVERR_SEQLEN
+    assert call(good, [0, 4, 3], [64, 40]) == lib.PKV_DEVERR_QUERY
+    assert call(good, [0, 0, 5], [64, 40]) == lib.PKV_DEVERR_QUERY  # 5 queries, max_query_len 4
+    assert call(good, [0, 2, 5], [64, 40]) == 0
+
+
+# ---------------------------------------------------------------- together
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_prompt_and_decode_steps_together(lib, q4):
+    """A prompt of two sequences, then decode steps: append with rotation, then attention, on one stream; every
+    step's output against the 64-bit definitions on the cache as it should stand."""
+    hq, hkv, d, window, sinks = 8, 2, 64, 48, 4
+    g = torch.Generator().manual_seed(11)
+    inv = 10000.0 ** -(torch.arange(0, d, 2, dtype=torch.float64) / d)
+    ang = torch.arange(256, dtype=torch.float64)[:, None] * inv
+    cs = torch.cat([ang.cos(), ang.sin()], 1).float()
+    table, blocks = sc.table_of(3, [160, 160], 10)
+    held = [np.zeros((blocks, hkv, 10 * d), np.uint8) if q4 else np.full((blocks * 16, hkv, d), np.nan) for _ in range(2)]
+    pools = [torch.from_numpy(h.copy()).cuda() if q4 else torch.from_numpy(h.copy()).bfloat16().cuda() for h in held]
+    lens = [0, 0]
+    for step in [(70, 33)] + [(1, 1)] * 5 + [(3, 1)] + [(0, 2)]:
+        qsl = np.array([0, step[0], sum(step)], np.int32)
+        pos = np.concatenate([np.arange(n, n + s) for n, s in zip(lens, step)]).astype(np.int32)
+        slots = np.concatenate([table[b][np.arange(lens[b], lens[b] + s) // 16].astype(np.int64) * 16
+                                + np.arange(lens[b], lens[b] + s) % 16 for b, s in enumerate(step)])
+        lens = [n + s for n, s in zip(lens, step)]
+        qkv = torch.randn(sum(step), hq + 2 * hkv, d, generator=g).bfloat16()
+        dev = qkv.cuda()
+        append, attend = ((lib.paged_kv_append_q4, lib.paged_attn_q4) if q4 else
+                          (lib.paged_kv_append, lib.paged_attn_window))
+        q = append(dev[:, :hq], dev[:, hq:hq + hkv], dev[:, hq + hkv:], torch.from_numpy(pos).cuda(), cs.cuda(),
+                   torch.from_numpy(slots).cuda(), *pools, flags=lib.PKV_CHECK_BOUNDS)
+        out = attend(q, *pools, torch.from_numpy(table).cuda(), torch.from_numpy(qsl).cuda(),
+                     torch.tensor(lens, dtype=torch.int32).cuda(), max(step), 160, d ** -0.5, window=window,
+                     sinks=sinks, flags=lib.PKV_CHECK_BOUNDS)
+        assert lib.check() == 0
+        turned = [rotated(qkv[:, a:b], torch.from_numpy(pos), cs, False) for a, b in ((0, hq), (hq, hq + hkv))]
+        if q4:
+            sv.q4_store(held[0], slots, turned[1][1])
+            sv.q4_store(held[1], slots, qkv[:, hq + hkv:].float().numpy())
+            k64, v64 = sv.q4_load(held[0]), sv.q4_load(held[1])
+        else:
+            held[0][slots], held[1][slots] = turned[1][0].double().numpy(), qkv[:, hq + hkv:].double().numpy()
+            k64, v64 = held
+        want, spread, reach = sv.window_attention(turned[0][0].double().numpy(), k64, v64, table, qsl, lens, d ** -0.5,
+                                                  window, sinks)
+        tol = sc.tolerance(want, spread, reach, 160, d, "bf16", 2.0 ** -8)
+        agree(out.double().cpu().numpy(), want, tol)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_captured_step_replays_with_new_contents(lib, q4):
+    """Append and attention captured once; replays follow the buffers' contents, two graphs on two streams agree."""
+    hq, hkv, d, B = 8, 2, 128, 3
+    g = torch.Generator().manual_seed(2)
+    rnd = lambda *s: torch.randn(*s, generator=g).bfloat16().cuda()  # noqa: E731
+    cs = torch.randn(64, d, generator=g).cuda()
+    table = torch.arange(B * 4, dtype=torch.int32).view(B, 4).cuda()
+    qsl = torch.arange(B + 1, dtype=torch.int32).cuda()
+
+    class State:
+        def __init__(self):
+            if q4:
+                self.kp, self.vp = (torch.from_numpy(sc.random_q4_pool(B * 4, hkv, d, s)).cuda() for s in (1, 2))
+            else:
+                gg = torch.Generator().manual_seed(9)
+                self.kp, self.vp = (torch.randn(B * 64, hkv, d, generator=gg).bfloat16().cuda() for _ in range(2))
+            self.q, self.out = torch.empty(B, hq, d).bfloat16().cuda(), torch.empty(B, hq, d).bfloat16().cuda()
+            self.qkv = torch.empty(B, hq + 2 * hkv, d).bfloat16().cuda()
+            self.pos, self.slots = torch.empty(B, dtype=torch.int32).cuda(), torch.empty(B, dtype=torch.int64).cuda()
+            self.lens = torch.empty(B, dtype=torch.int32).cuda()
+
+        def load(self, qkv, lens):
+            self.qkv.copy_(qkv)
+            self.lens.copy_(lens)
+            self.pos.copy_(lens - 1)
+            at = (lens - 1).long()
+            self.slots.copy_(table.long().gather(1, (at // 16)[:, None])[:, 0] * 16 + at % 16)
+
+        def step(self):
+            append, attend = ((lib.paged_kv_append_q4, lib.paged_attn_q4) if q4 else
+                              (lib.paged_kv_append, lib.paged_attn_window))
+            append(self.qkv[:, :hq], self.qkv[:, hq:hq + hkv], self.qkv[:, hq + hkv:], self.pos, cs, self.slots,
+                   self.kp, self.vp, q_out=self.q)
+            attend(self.q, self.kp, self.vp, table, qsl, self.lens, 1, 64, 0.1, window=30, sinks=3, out=self.out)
+
+    eager, graphs, states = State(), [], [State(), State()]
+    first = torch.tensor([20, 41, 5], dtype=torch.int32).cuda()
+    x = rnd(B, hq + 2 * hkv, d)
+    for s in states:
+        s.load(x, first)
+        s.step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            s.step()
+        graphs.append(graph)
+    eager.load(x, first)
+    eager.step()
+    for n in range(3):
+        x, lens = rnd(B, hq + 2 * hkv, d), first + n + 1
+        eager.load(x, lens)
+        eager.step()
+        for s in states:
+            s.load(x, lens)
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in graphs]
+        for st, graph in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+        for s in states:
+            assert torch.equal(s.out, eager.out) and torch.equal(s.kp, eager.kp) and torch.equal(s.q, eager.q)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_repeated_calls_give_the_same_bits(lib, q4):
+    a = attention(lib, [(1, 3000), (2, 900)], 8, 2, 128, "bf16", 0, 0, q4, seed=3, poison=False)[0]
+    for _ in range(3):
+        assert np.array_equal(a, attention(lib, [(1, 3000), (2, 900)], 8, 2, 128, "bf16", 0, 0, q4, seed=3, poison=False)[0])
