@@ -26,7 +26,7 @@ LIB = os.path.join(PKG, "libpagedkv.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_SOURCES = ["device.cu", "kv_write.cu", "attn_simt.cu", "attn_tc.cu", "noalloc.cu", "selftest.cu", "serving.cu",
-                "kv_append.cu", "attn_win_simt.cu"]
+                "kv_append.cu", "attn_win_simt.cu", "attn_win_dec.cu"]
 HOST_SOURCES = ["host.cpp"]
 
 

@@ -125,6 +125,7 @@ int pkv_launch_append(const PkvAppendArgs& a, pkv_dtype dt, bool q4, void* strea
 int pkv_launch_gather_q4(const void* kp, const void* vp, int64_t num_blocks, const int32_t* table, int B, int W,
                          int first_block, int n_blocks, void* sk, void* sv, int64_t stage_rows, int Hkv, int D,
                          pkv_dtype dt, unsigned int* err, int check, void* stream);
+int pkv_launch_win_dec(const PkvWinArgs& a, pkv_dtype dt, int D, bool q4, void* stream);
 int pkv_launch_win_simt(const PkvWinArgs& a, pkv_dtype dt, int D, bool q4, void* stream);
 
 // Shared by those launchers (serving.cu).

@@ -103,7 +103,8 @@ pkv_status win_impl(const char* fn, bool q4, const void* q, int64_t Tq, int Hq, 
   a.scale = softmax_scale;
   a.err = pkv_device_error_word();
   if (!a.err) return pkv_fail(PKV_ERR_CUDA, "%s: device error word unavailable", fn);
-  const int rc = pkv_launch_win_simt(a, dt, D, q4, stream);
+  const bool simt = dt == PKV_F32 || (flags & PKV_FORCE_SIMT);
+  const int rc = simt ? pkv_launch_win_simt(a, dt, D, q4, stream) : pkv_launch_win_dec(a, dt, D, q4, stream);
   if (rc) return pkv_fail(PKV_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString((cudaError_t)rc));
   pkv_set_launches(1);
   return PKV_OK;
