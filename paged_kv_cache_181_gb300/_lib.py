@@ -402,66 +402,113 @@ def q4_block_bytes(head_dim: int) -> int:
     return n
 
 
+# These calls are a few microseconds of GPU time in a decode step, so their argument checks are written for few
+# interpreter steps: one pass over the tensors, the raw stream handle, no temporary objects.  (Through the helpers
+# above a call took 18 us of host time.)
+_DTYPES: dict = {}
+_raw_stream = _current_device = None
+
+
+def _init_fast() -> None:
+    global _raw_stream, _current_device
+    torch = _torch()
+    _DTYPES.update({torch.float32: PKV_F32, torch.bfloat16: PKV_BF16, torch.float16: PKV_F16})
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _code(fn: str, dtype) -> int:
+    if not _DTYPES:
+        _init_fast()
+    c = _DTYPES.get(dtype)
+    if c is None:
+        raise ValueError(f"{fn}: {dtype} is not supported")
+    return c
+
+
+def _check_device(fn: str, tensors) -> int:
+    """Every tensor contiguous and on the current CUDA device; returns the device's index."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev or not t.is_contiguous() or dev < 0:
+            if not t.is_cuda:
+                raise ValueError(f"{fn}: tensors must be on a CUDA device (got {t.device})")
+            if not t.is_contiguous():
+                raise ValueError(f"{fn}: tensors must be contiguous")
+            raise ValueError(f"{fn}: tensors must be on one CUDA device (got {tensors[0].device} and {t.device})")
+    if dev != _current_device():
+        raise ValueError(f"{fn}: tensors are on cuda:{dev}, the current device is cuda:{_current_device()}")
+    return dev
+
+
 def _token_stride(fn: str, name: str, x) -> int:
     """Elements between the tokens of ``x [T, H, D]``, whose heads and channels must be contiguous."""
     T, h, d = x.shape
     st, sh, sd = x.stride()
     if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{fn}: {name}'s heads and channels must be contiguous (strides {tuple(x.stride())})")
-    if T <= 1:
-        return h * d
-    if st < 0:
-        raise ValueError(f"{fn}: {name} has a negative token stride")
-    return st
+    return st if T > 1 else h * d
 
 
 def _append(fn: str, entry, q4: bool, q, k, v, positions, cos_sin, slot_mapping, key_pool, value_pool, interleaved,
             q_out, flags, stream):
     torch = _torch()
-    if k.dim() != 3 or v.shape != k.shape:
+    shape, dtype = k.shape, k.dtype
+    code = _code(fn, dtype)
+    if len(shape) != 3 or v.shape != shape:
         raise ValueError(f"{fn}: k and v must be [T, Hkv, D]")
-    T, hkv, d = k.shape
-    hq = 0
+    T, hkv, d = shape
+    if v.dtype != dtype:
+        raise ValueError(f"{fn}: q, k, v and q_out must share one dtype")
+    hq = q_at = q_stride = q_out_at = 0
+    pool_shape = key_pool.shape
+    if len(pool_shape) != 3 or value_pool.shape != pool_shape:
+        raise ValueError(f"{fn}: the pools must be 3-D and of one shape")
+    tensors = [key_pool, value_pool, slot_mapping]
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d:
+        q_shape = q.shape
+        if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != d:
             raise ValueError(f"{fn}: q must be [T, Hq, D]")
-        hq = q.shape[1]
+        hq = q_shape[1]
         if q_out is None:
-            q_out = torch.empty((T, hq, d), dtype=q.dtype, device=q.device)
-        elif q_out.shape != q.shape:
-            raise ValueError(f"{fn}: q_out shape {tuple(q_out.shape)} differs from q {tuple(q.shape)}")
+            q_out = torch.empty(q_shape, dtype=q.dtype, device=q.device)
+        elif q_out.shape != q_shape:
+            raise ValueError(f"{fn}: q_out shape {tuple(q_out.shape)} differs from q {tuple(q_shape)}")
+        if q.dtype != dtype or q_out.dtype != dtype:
+            raise ValueError(f"{fn}: q, k, v and q_out must share one dtype")
+        q_at, q_stride, q_out_at = q.data_ptr(), _token_stride(fn, "q", q), q_out.data_ptr()
+        tensors.append(q_out)
     elif q_out is not None:
         raise ValueError(f"{fn}: q_out given without q")
-    if key_pool.shape != value_pool.shape or key_pool.dim() != 3:
-        raise ValueError(f"{fn}: the pools must be 3-D and of one shape")
-    if q4:
-        if key_pool.shape[1:] != (hkv, q4_block_bytes(d)):
-            raise ValueError(f"{fn}: the pools must be [num_blocks, {hkv}, {q4_block_bytes(d)}]")
-        if key_pool.dtype != torch.uint8 or value_pool.dtype != torch.uint8:
-            raise ValueError(f"{fn}: 4-bit pools are uint8")
-    elif key_pool.shape[1:] != (hkv, d):
-        raise ValueError(f"{fn}: the pools must be [num_slots, {hkv}, {d}]")
-    elif key_pool.dtype != k.dtype or value_pool.dtype != k.dtype:
-        raise ValueError(f"{fn}: sources and pools must share one dtype")
-    if v.dtype != k.dtype or (q is not None and (q.dtype != k.dtype or q_out.dtype != k.dtype)):
-        raise ValueError(f"{fn}: q, k, v and q_out must share one dtype")
+    _, pool_heads, width = pool_shape
+    if pool_heads != hkv or width != (10 * d if q4 else d):
+        raise ValueError(f"{fn}: the pools must be [{'num_blocks' if q4 else 'num_slots'}, {hkv}, {10 * d if q4 else d}]")
+    pool_dtype = torch.uint8 if q4 else dtype
+    if key_pool.dtype != pool_dtype or value_pool.dtype != pool_dtype:
+        raise ValueError(f"{fn}: 4-bit pools are uint8" if q4 else f"{fn}: sources and pools must share one dtype")
     if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
         raise ValueError(f"{fn}: slot_mapping must be int64 [T]")
-    rot, max_position = 0, 0
+    rot = max_position = pos_at = cs_at = 0
     if cos_sin is not None:
         if positions is None or positions.dtype != torch.int32 or positions.numel() != T:
             raise ValueError(f"{fn}: positions must be int32 [T]")
-        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
             raise ValueError(f"{fn}: cos_sin must be float32 [max_position, rot_dim]")
         max_position, rot = cos_sin.shape
-    _require(fn, slot_mapping, q_out, key_pool, value_pool, positions if rot else None, cos_sin if rot else None)
-    for x in (q, k, v):
-        if x is not None and x.device != key_pool.device:
-            raise ValueError(f"{fn}: tensors must be on one CUDA device (got {x.device})")
-    _ok(entry(_dptr(q), 0 if q is None else _token_stride(fn, "q", q), _dptr(k), _token_stride(fn, "k", k), _dptr(v),
-              _token_stride(fn, "v", v), _dptr(positions) if rot else 0, _dptr(cos_sin) if rot else 0, max_position,
-              rot, _dptr(slot_mapping), T, hq, _dptr(q_out), _dptr(key_pool), _dptr(value_pool), key_pool.shape[0],
-              hkv, d, dtype_code(k), flags | (PKV_ROPE_INTERLEAVED if interleaved else 0), _stream(stream)))
+        if rot:
+            pos_at, cs_at = positions.data_ptr(), cos_sin.data_ptr()
+            tensors += (positions, cos_sin)
+    dev = _check_device(fn, tensors)
+    if k.get_device() != dev or v.get_device() != dev or (hq and q.get_device() != dev):
+        raise ValueError(f"{fn}: tensors must be on one CUDA device")
+    status = entry(q_at, q_stride, k.data_ptr(), _token_stride(fn, "k", k), v.data_ptr(), _token_stride(fn, "v", v),
+                   pos_at, cs_at, max_position, rot, slot_mapping.data_ptr(), T, hq, q_out_at, key_pool.data_ptr(),
+                   value_pool.data_ptr(), pool_shape[0], hkv, d, code,
+                   flags | PKV_ROPE_INTERLEAVED if interleaved else flags,
+                   _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _ok(status)
     return q_out
 
 
@@ -487,57 +534,69 @@ def paged_kv_gather_q4(key_pool, value_pool, block_table, stage_k, stage_v, *, f
                        n_blocks: int | None = None, flags: int = 0, stream=None) -> None:
     """The values of table blocks [first_block, first_block + n_blocks) of every row, into ``stage_k/v [B, rows, Hkv, D]``."""
     fn, torch = "paged_kv_gather_q4", _torch()
-    if block_table.dim() != 2 or stage_k.dim() != 4 or key_pool.dim() != 3:
+    code = _code(fn, stage_k.dtype)
+    shape, pool_shape = stage_k.shape, key_pool.shape
+    if block_table.dim() != 2 or len(shape) != 4 or len(pool_shape) != 3:
         raise ValueError(f"{fn}: block_table must be [B, W], staging [B, rows, Hkv, D], pools [num_blocks, Hkv, bytes]")
     B, W = block_table.shape
-    hkv, d = stage_k.shape[2:]
+    rows_b, rows, hkv, d = shape
     if n_blocks is None:
         n_blocks = W - first_block
-    if stage_v.shape != stage_k.shape or stage_k.shape[0] != B or stage_v.dtype != stage_k.dtype:
+    if rows_b != B or stage_v.shape != shape or stage_v.dtype != stage_k.dtype:
         raise ValueError(f"{fn}: staging buffers must be [B, rows, Hkv, D], of one dtype")
-    if key_pool.shape != value_pool.shape or key_pool.shape[1:] != (hkv, q4_block_bytes(d)):
-        raise ValueError(f"{fn}: the pools must be [num_blocks, {hkv}, {q4_block_bytes(d)}]")
+    if value_pool.shape != pool_shape or pool_shape[1] != hkv or pool_shape[2] != 10 * d:
+        raise ValueError(f"{fn}: the pools must be [num_blocks, {hkv}, {10 * d}]")
     if key_pool.dtype != torch.uint8 or value_pool.dtype != torch.uint8:
         raise ValueError(f"{fn}: 4-bit pools are uint8")
-    _require(fn, key_pool, value_pool, block_table, stage_k, stage_v)
-    _require_metadata(fn, block_table)
-    _ok(lib.paged_kv_gather_q4(_dptr(key_pool), _dptr(value_pool), key_pool.shape[0], _dptr(block_table), B, W,
-                               int(first_block), int(n_blocks), _dptr(stage_k), _dptr(stage_v), stage_k.shape[1], hkv,
-                               d, dtype_code(stage_k), flags, _stream(stream)))
+    if block_table.dtype != torch.int32:
+        raise ValueError(f"{fn}: block_table must be int32")
+    dev = _check_device(fn, (key_pool, value_pool, block_table, stage_k, stage_v))
+    status = lib.paged_kv_gather_q4(key_pool.data_ptr(), value_pool.data_ptr(), pool_shape[0], block_table.data_ptr(),
+                                    B, W, int(first_block), int(n_blocks), stage_k.data_ptr(), stage_v.data_ptr(), rows,
+                                    hkv, d, code, flags, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _ok(status)
 
 
 def _attn_window(fn: str, entry, q4: bool, q, key_pool, value_pool, block_table, query_start_loc, seq_lens,
                  max_query_len, max_seq_len, softmax_scale, window, sinks, out, flags, block_size, stream):
     torch = _torch()
-    if q.dim() != 3 or key_pool.dim() != 3 or block_table.dim() != 2:
+    shape, dtype, pool_shape, table_shape = q.shape, q.dtype, key_pool.shape, block_table.shape
+    code = _code(fn, dtype)
+    if len(shape) != 3 or len(pool_shape) != 3 or len(table_shape) != 2:
         raise ValueError(f"{fn}: q must be [Tq, Hq, D], the pools 3-D and block_table [B, W]")
-    Tq, hq, d = q.shape
-    B, W = block_table.shape
-    hkv = key_pool.shape[1]
-    if value_pool.shape != key_pool.shape:
-        raise ValueError(f"{fn}: value_pool shape {tuple(value_pool.shape)} differs from key_pool {tuple(key_pool.shape)}")
+    Tq, hq, d = shape
+    B, W = table_shape
+    blocks, hkv, width = pool_shape
+    if value_pool.shape != pool_shape:
+        raise ValueError(f"{fn}: value_pool shape {tuple(value_pool.shape)} differs from key_pool {tuple(pool_shape)}")
     if q4:
-        if key_pool.shape[2] != q4_block_bytes(d):
-            raise ValueError(f"{fn}: the pools must be [num_blocks, Hkv, {q4_block_bytes(d)}]")
-        num_blocks, pool_dtype = key_pool.shape[0], torch.uint8
+        if width != 10 * d:
+            raise ValueError(f"{fn}: the pools must be [num_blocks, Hkv, {10 * d}]")
+        pool_dtype = torch.uint8
     else:
-        if key_pool.shape[2] != d or key_pool.shape[0] % block_size:
+        if width != d or block_size <= 0 or blocks % block_size:
             raise ValueError(f"{fn}: the pools must be [num_blocks * {block_size}, Hkv, {d}]")
-        num_blocks, pool_dtype = key_pool.shape[0] // block_size, q.dtype
+        blocks, pool_dtype = blocks // block_size, dtype
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != q.shape:
-        raise ValueError(f"{fn}: out shape {tuple(out.shape)} differs from q {tuple(q.shape)}")
+    elif out.shape != shape:
+        raise ValueError(f"{fn}: out shape {tuple(out.shape)} differs from q {tuple(shape)}")
     if query_start_loc.numel() != B + 1 or seq_lens.numel() != B:
         raise ValueError(f"{fn}: query_start_loc must hold B+1 = {B + 1} and seq_lens B = {B} entries "
                          f"(got {query_start_loc.numel()} and {seq_lens.numel()})")
-    _require(fn, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, out)
-    if key_pool.dtype != pool_dtype or value_pool.dtype != pool_dtype or out.dtype != q.dtype:
+    if key_pool.dtype != pool_dtype or value_pool.dtype != pool_dtype or out.dtype != dtype:
         raise ValueError(f"{fn}: the pools must be {pool_dtype} and out of q's dtype")
-    _require_metadata(fn, block_table, query_start_loc, seq_lens)
-    _ok(entry(_dptr(q), Tq, hq, _dptr(key_pool), _dptr(value_pool), num_blocks, block_size, hkv, d, dtype_code(q),
-              _dptr(block_table), B, W, _dptr(query_start_loc), _dptr(seq_lens), int(max_query_len), int(max_seq_len),
-              float(softmax_scale), int(window), int(sinks), _dptr(out), flags, _stream(stream)))
+    i32 = torch.int32
+    if block_table.dtype != i32 or query_start_loc.dtype != i32 or seq_lens.dtype != i32:
+        raise ValueError(f"{fn}: metadata must be int32")
+    dev = _check_device(fn, (q, key_pool, value_pool, block_table, query_start_loc, seq_lens, out))
+    status = entry(q.data_ptr(), Tq, hq, key_pool.data_ptr(), value_pool.data_ptr(), blocks, block_size, hkv, d, code,
+                   block_table.data_ptr(), B, W, query_start_loc.data_ptr(), seq_lens.data_ptr(), int(max_query_len),
+                   int(max_seq_len), float(softmax_scale), int(window), int(sinks), out.data_ptr(), flags,
+                   _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _ok(status)
     return out
 
 

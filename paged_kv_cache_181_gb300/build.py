@@ -26,7 +26,7 @@ LIB = os.path.join(PKG, "libpagedkv.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_SOURCES = ["device.cu", "kv_write.cu", "attn_simt.cu", "attn_tc.cu", "noalloc.cu", "selftest.cu", "serving.cu",
-                "kv_append.cu", "attn_win_simt.cu", "attn_win_dec.cu"]
+                "kv_append.cu", "attn_win_simt.cu", "attn_win_dec.cu", "attn_win_tc.cu"]
 HOST_SOURCES = ["host.cpp"]
 
 
@@ -57,10 +57,12 @@ def _run(cmd: list[str], verbose: bool, log: str | None = None) -> str:
 # bf16/f16 call at run time (the launcher keeps the same check as a backstop).
 TC_SOURCE = "attn_tc.cu"
 TC_KERNEL = "attn_tc_kernel"
+WIN_TC_SOURCE = "attn_win_tc.cu"  # the window/sinks kernel splits its registers the same way
+WIN_TC_KERNEL = "attn_win_tc_kernel"
 # Sources whose ptxas report is kept beside their object (`<source>.ptxas.txt`): the tensor-core kernel's for
 # the gate below, the CUDA-core kernel's for its spill check (it runs at 252-254 registers, where a
-# toolchain that allocated differently would start spilling: slower, not wrong).
-PTXAS_LOGGED = (TC_SOURCE, "attn_simt.cu")
+# toolchain that allocated differently would start spilling: slower, not wrong), and the window kernels' for both.
+PTXAS_LOGGED = (TC_SOURCE, "attn_simt.cu", "attn_win_tc.cu", "attn_win_dec.cu")
 
 
 def expected_tc_registers(source: str) -> int:
@@ -70,8 +72,8 @@ def expected_tc_registers(source: str) -> int:
     return int(m.group(1))
 
 
-def check_tc_registers(ptxas_log: str, expected: int) -> int:
-    """Every instantiation of the tensor-core kernel in a ``-Xptxas -v`` log uses ``expected`` registers;
+def check_tc_registers(ptxas_log: str, expected: int, kernel: str = TC_KERNEL, source: str = TC_SOURCE) -> int:
+    """Every instantiation of a tensor-core kernel in a ``-Xptxas -v`` log uses ``expected`` registers;
     returns how many instantiations were checked, raises RuntimeError otherwise."""
     seen = 0
     current = None
@@ -82,16 +84,16 @@ def check_tc_registers(ptxas_log: str, expected: int) -> int:
             continue
         m = re.search(r"Used (\d+) registers", line)
         if m and current is not None:
-            if TC_KERNEL in current:
+            if kernel in current:
                 seen += 1
                 if int(m.group(1)) != expected:
                     raise RuntimeError(
-                        f"{TC_SOURCE}: {current} compiled to {m.group(1)} registers per thread, but its warpgroup "
+                        f"{source}: {current} compiled to {m.group(1)} registers per thread, but its warpgroup "
                         f"register split (setmaxnreg) is sized for {expected}; adjust kLaunchRegs/kRegsLow/"
                         f"kRegsHigh or the kernel's register use")
             current = None
     if seen == 0:
-        raise RuntimeError(f"{TC_SOURCE}: no register report for {TC_KERNEL} in the ptxas output")
+        raise RuntimeError(f"{source}: no register report for {kernel} in the ptxas output")
     return seen
 
 
@@ -127,7 +129,6 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
     headers.append(os.path.join(INCLUDE, "pagedkv.h"))
     jobs = []
     objs = []
-    tc_log = os.path.join(OUT_DIR, TC_SOURCE + ".ptxas.txt")
     for src in CUDA_SOURCES:
         path = os.path.join(CSRC, src)
         obj = os.path.join(OUT_DIR, src + ".o")
@@ -150,11 +151,14 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             for f in [ex.submit(_run, cmd, verbose, log) for cmd, log in jobs]:
                 f.result()
-    with open(os.path.join(CSRC, TC_SOURCE)) as f:
-        expected = expected_tc_registers(f.read())
-    with open(tc_log) as f:
+    for source, kernel in ((TC_SOURCE, TC_KERNEL), (WIN_TC_SOURCE, WIN_TC_KERNEL)):
+        tc_log = os.path.join(OUT_DIR, source + ".ptxas.txt")
+        with open(os.path.join(CSRC, source)) as f:
+            expected = expected_tc_registers(f.read())
+        with open(tc_log) as f:
+            log = f.read()
         try:
-            check_tc_registers(f.read(), expected)
+            check_tc_registers(log, expected, kernel, source)
         except RuntimeError:
             os.remove(tc_log)  # the next build compiles the kernel again
             raise

@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_win_dec_kernel
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e2 = top > 0.f && top <= 3.402823466e38f ? 13 - ilogbf(top) : 0;
+      const int e2 = top > 0.f && top <= 3.402823466e38f ? min(13 - ilogbf(top), 64) : 0;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const T* e = reinterpret_cast<const T*>(&x[i]);
@@ -478,13 +478,14 @@ int launch(const PkvWinArgs& a, cudaStream_t s) {
   constexpr int PF = POOLQ4 ? 2 : 1;
   auto kernel = attn_win_dec_kernel<T, POOLQ4, D, NT, PF>;
   const size_t smem = sizeof(DecSmem<D, NT>);
-  static std::atomic<uint64_t> attr_set[64];
-  const int rc = pkv_prepare_kernel((const void*)kernel, (int)smem, attr_set);
+  static PkvKernelState state;
+  const int rc = pkv_prepare_kernel((const void*)kernel, (int)smem, kThreads, 0, state);
   if (rc) return rc;
   const int g = a.Hq / a.Hkv;
   const int64_t items = (int64_t)a.B * a.Hkv * (((int64_t)a.max_query_len * g + 8 * NT - 1) / (8 * NT));
-  const int ctas = pkv_plan_cluster(items, pkv_visible_keys(a, 8 * NT / g + 1) / (16 * kWarps) + 1, NT == 1 ? 3 : 2);
-  return pkv_launch_cluster((const void*)kernel, items, ctas, kThreads, smem, &a, s);
+  const int ctas = pkv_plan_cluster(state, items, pkv_visible_keys(a, 8 * NT / g + 1) / (16 * kWarps) + 1, 4.0);
+  void* args[] = {const_cast<PkvWinArgs*>(&a)};
+  return pkv_launch_cluster((const void*)kernel, items, ctas, kThreads, smem, args, s);
 }
 
 template <typename T, bool POOLQ4, int D>

@@ -175,13 +175,14 @@ template <typename T, typename Pool, int D>
 int launch(const PkvWinArgs& a, cudaStream_t s) {
   auto kernel = attn_win_simt_kernel<T, Pool, D>;
   const size_t smem = sizeof(Smem<D>);
-  static std::atomic<uint64_t> attr_set[64];
-  const int rc = pkv_prepare_kernel((const void*)kernel, (int)smem, attr_set);
+  static PkvKernelState state;
+  const int rc = pkv_prepare_kernel((const void*)kernel, (int)smem, kThreads, 0, state);
   if (rc) return rc;
   const int g = a.Hq / a.Hkv;
   const int64_t items = (int64_t)a.B * a.Hkv * (((int64_t)a.max_query_len * g + kRows - 1) / kRows);
-  const int ctas = pkv_plan_cluster(items, pkv_visible_keys(a, kRows / g + 1) / kKeys + 1, 3);
-  return pkv_launch_cluster((const void*)kernel, items, ctas, kThreads, smem, &a, s);
+  const int ctas = pkv_plan_cluster(state, items, pkv_visible_keys(a, kRows / g + 1) / kKeys + 1, 2.0);
+  void* args[] = {const_cast<PkvWinArgs*>(&a)};
+  return pkv_launch_cluster((const void*)kernel, items, ctas, kThreads, smem, args, s);
 }
 
 template <typename T, typename Pool>

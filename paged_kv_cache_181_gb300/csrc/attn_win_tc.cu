@@ -1,0 +1,724 @@
+// Window/sinks attention for many query rows per kv head (prompts and prompt chunks), bf16/f16 queries over 16-bit
+// or 4-bit pools: tcgen05 products with TMEM accumulators, fp32 online softmax.
+//
+// One CTA = two 128-row tiles of packed query rows (attn_win.cuh: floor(128 / g) tokens x g heads of one kv head a
+// tile), which share every key and value tile.  Packing the heads that share keys shortens the stretch of
+// positions a tile spans, and with it the keys that only some of its rows see: with a window of 1024 and g = 4, 256
+// rows are 64 positions and visit 1024 + 64 keys, where 256 positions of one head would visit 1024 + 256.
+// The CTAs of a cluster take parts of an item's key tiles and merge through shared memory: it evens out the last
+// wave and fills the GPU when there are few items.
+//
+// Key tiles are eight of the pages that some row sees (WinPages), so the keys between the sinks and the window are
+// skipped at page granularity; what a row does not see inside a page is masked in its scores.  Values that no row
+// sees are zero in shared memory (0 * NaN would not be).
+//
+// Warps: 1 issues the MMAs and owns TMEM; 4-7 and 8-11 are the softmax of the two tiles, one row per thread; and
+//   16-bit pools: 0 loads Q and the key tiles by TMA (one box per page), 3 the value tiles;
+//   4-bit pools:  0, 2 and 3 read codes, turn them into the fp16 numbers they stand for and store them swizzled as
+//                 TMA would; Q is converted to fp16 by the softmax threads, each row scaled by a power of two.
+//                 Channels of a code word come out as (0,4), (1,5), (2,6), (3,7): Q's and the output's channels are
+//                 permuted to match, which is free, instead of the codes.
+// The order of MMAs, the ring of slots shared by key and value tiles, the lazy rescale and the register split between
+// warpgroups are those of the prefix-mask kernel (attn_tc.cu), which says why.
+// Every mbarrier wait is bounded in time (1 s); on expiry the CTA records PKV_DEVERR_TIMEOUT and unwinds.
+
+#include <cuda.h>
+
+#include <atomic>
+#include <cstring>
+#include <mutex>
+#include <type_traits>
+
+#include "attn_win.cuh"
+#include "q4.cuh"
+#include "tc_ptx.cuh"
+
+namespace {
+
+constexpr int BM = 128;  // rows per tile; two tiles per CTA
+constexpr int BN = 128;  // keys per tile
+constexpr int kPages = BN / 16;
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168;  // registers per thread the kernel is compiled to (checked at launch)
+constexpr int kRegsLow = 104, kRegsHigh = 200;
+static_assert(128 * kRegsLow + 256 * kRegsHigh == kThreads * kLaunchRegs, "register split must add up");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint64_t kWaitLimitNs = 1000000000ull;
+constexpr float kRescale = 8.f;  // log2 units
+constexpr int kDequantWarps = 3;
+
+template <int D>
+struct Cfg {
+  static constexpr int TILE = BN * D * 2;
+  static constexpr int NSLOT = D == 128 ? 5 : 10;
+  static constexpr int GS = (D / 64) * 1024;  // stride of 8-row atoms in a key/value tile
+  static constexpr int OSTRIDE = D + 4;       // floats between rows staged for the merge
+};
+
+template <int D>
+struct alignas(1024) WinSmem {
+  uint8_t q[2][BM * D * 2];                 // [D/64][128 rows][128 B] per tile, 128-byte swizzled
+  uint8_t kv[Cfg<D>::NSLOT][Cfg<D>::TILE];  // [page][8-row group][column half][8 rows][128 B], swizzled
+  uint64_t full[Cfg<D>::NSLOT], empty[Cfg<D>::NSLOT];
+  uint64_t q_full, s_full[2], p_full[2], mma_done;
+  uint32_t tmem_base;
+  int abort, skip;
+};
+static_assert(sizeof(WinSmem<128>) + 1024 <= 227 * 1024, "shared memory of a CTA");
+static_assert(2 * BM * Cfg<128>::OSTRIDE * 4 <= sizeof(WinSmem<128>::kv), "merge rows fit the ring");
+static_assert(2 * BM * Cfg<64>::OSTRIDE * 4 <= sizeof(WinSmem<64>::kv), "merge rows fit the ring");
+
+struct WinMaps {
+  CUtensorMap q, o;    // (D, g, Hkv, Tq), box = 64 columns x g heads x a tile's tokens
+  CUtensorMap kb, vb;  // pools as (64, 8, D/64, slots/8, Hkv), box = one 16-row page of one head
+  CUtensorMap v1;      // pool as (D, Hkv, slots), box = 64 columns of one row
+};
+
+template <int D>
+__host__ __device__ constexpr int row_offset(int r, int dh) {
+  return (r >> 4) * (2 * Cfg<D>::GS) + ((r >> 3) & 1) * Cfg<D>::GS + dh * 1024 + (r & 7) * 128;
+}
+
+PKV_DEVINLINE void tma_load_4d(void* dst, const void* tmap, int c0, int c1, int c2, int c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(ptx::smem_u32(dst)),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(ptx::smem_u32(bar))
+      : "memory");
+}
+PKV_DEVINLINE void tma_store_4d(const void* tmap, int c0, int c1, int c2, int c3, const void* src) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(tmap),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(ptx::smem_u32(src))
+               : "memory");
+}
+
+template <int D>
+PKV_DEVINLINE void note_abort(WinSmem<D>& sm, unsigned int* err) {
+  sm.abort = 1;
+  pkv_raise(err, PKV_DEVERR_TIMEOUT);
+}
+
+PKV_DEVINLINE bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int lane) {
+  bool ok = true;
+  if (lane == 0) ok = ptx::mbar_wait(bar, parity, abort, kWaitLimitNs);
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// One warp loads a 16-bit key or value tile: pages [8 kt, 8 kt + 8) of the item's list, a lane per page.
+template <int D>
+PKV_DEVINLINE void load_tile(uint8_t* dst, const WinMaps& maps, bool is_v, uint64_t* full, const PkvWinArgs& a,
+                             const WinPages& pg, int b, int kvh, int kt, int lane) {
+  const int v = kPages * kt + lane;
+  const bool there = lane < kPages && v < pg.n;
+  const int page = there ? pg.page(v) : 0;
+  const int blk = there ? win_block(a, b, page) : 0;
+  unsigned seen = there ? 0xffffu : 0u;  // rows of the page that some query sees
+  if (is_v) {
+    if (there) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (!pg.any(page * 16 + r)) seen &= ~(1u << r);
+    }
+    // Unseen value rows are zeroed; whole 128-byte rows, so the swizzle does not matter.
+    bool cleared = false;
+    for (int k = 0; k < kPages; ++k) {
+      const unsigned bits = __shfl_sync(0xffffffffu, seen, k);
+      if (bits == 0xffffu) continue;
+      cleared = true;
+      for (int e = lane; e < 16 * (D / 64) * 8; e += 32) {
+        const int c = e & 7, dh = (e >> 3) % (D / 64), r = (e >> 3) / (D / 64);
+        if (!((bits >> r) & 1))
+          *reinterpret_cast<uint4*>(dst + row_offset<D>(16 * k + r, dh) + c * 16) = make_uint4(0, 0, 0, 0);
+      }
+    }
+    if (cleared) ptx::fence_proxy_async_smem();
+    __syncwarp();
+  }
+  const int rows = __reduce_add_sync(0xffffffffu, __popc(seen));
+  if (lane == 0) ptx::mbar_arrive_expect_tx(full, (uint32_t)(rows * D * 2));
+  __syncwarp();
+  if (seen == 0xffffu) {
+    ptx::tma_load_5d(dst + row_offset<D>(16 * lane, 0), is_v ? &maps.vb : &maps.kb, 0, 0, 0, blk * 2, kvh, full);
+  } else if (seen) {
+    for (int r = 0; r < 16; ++r)
+      if ((seen >> r) & 1)
+#pragma unroll
+        for (int dh = 0; dh < D / 64; ++dh)
+          ptx::tma_load_3d(dst + row_offset<D>(16 * lane + r, dh), &maps.v1, dh * 64, kvh, blk * 16 + r, full);
+  }
+}
+
+// A lane's piece of a 4-bit tile: 32 channels (one group) of one key.
+struct Q4Piece {
+  uint4 code;
+  uint32_t pair;
+};
+
+template <int D, typename T, bool OPBF16, bool POOLQ4>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_win_tc_kernel(const __grid_constant__ WinMaps maps, const PkvWinArgs a) {
+  using C = Cfg<D>;
+  constexpr bool OUTBF16 = !std::is_same<T, __half>::value;
+  extern __shared__ uint8_t smem_raw[];
+  WinSmem<D>& sm = *reinterpret_cast<WinSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = a.Hq / a.Hkv;
+  const int TM = BM / g;  // tokens per tile
+  const uint32_t rank = cluster_rank(), n_cta = cluster_size();
+  // Items with the latest queries (the most keys) first; the kv heads of one stretch of queries run together.
+  uint32_t item = blockIdx.x / n_cta;
+  const int n_qp = (a.max_query_len + 2 * TM - 1) / (2 * TM);
+  const int kvh = item % a.Hkv;
+  item /= a.Hkv;
+  const int b = item % a.B, qp = n_qp - 1 - item / a.B;
+  const WinRow row = win_row(a, b, tid == 0 && qp == 0 && kvh == 0 && rank == 0);
+  const int i0 = qp * 2 * TM;
+  if (i0 >= row.Sq) return;  // the whole cluster leaves
+  const int n_q = i0 + TM < row.Sq ? 2 : 1;
+  const int base = row.L - row.Sq;
+  const int last = row.Sq < i0 + 2 * TM ? row.Sq : i0 + 2 * TM;  // one past the CTA's last token
+  const WinPages pg = win_pages(base + i0, base + last - 1, a.window, a.sinks);
+  const int n_tiles = (pg.n + kPages - 1) / kPages;
+  const int per = (n_tiles + (int)n_cta - 1) / (int)n_cta;
+  const int t_begin = (int)rank * per;
+  const int t_end = n_tiles < t_begin + per ? n_tiles : t_begin + per;
+  int n = t_end > t_begin ? t_end - t_begin : 0;
+
+  const int grp = warp >= 8 ? 1 : 0;
+  const bool is_softmax = warp >= 4;
+  const int quarter = warp & 3;
+  const int trow = quarter * 32 + lane;             // row of the tile
+  const int tok = i0 + grp * TM + trow / g;         // local query token of the row
+  const bool valid = is_softmax && trow < TM * g && tok < row.Sq;
+  float sl2 = a.scale * 1.4426950408889634f;
+
+  if (tid == 0) {
+    for (int s = 0; s < C::NSLOT; ++s) {
+      ptx::mbar_init(&sm.full[s], POOLQ4 ? kDequantWarps : 1);
+      ptx::mbar_init(&sm.empty[s], 1);
+    }
+    ptx::mbar_init(&sm.q_full, 1);
+    for (int w = 0; w < 2; ++w) {
+      ptx::mbar_init(&sm.s_full[w], 1);
+      ptx::mbar_init(&sm.p_full[w], 128);
+    }
+    ptx::mbar_init(&sm.mma_done, 1);
+    sm.abort = 0;
+    // After a pipeline timeout in an earlier launch results are invalid: do not wait for it again.
+    sm.skip = (*(volatile unsigned int*)a.err & PKV_DEVERR_TIMEOUT) != 0;
+    ptx::fence_mbar_init();
+    if (POOLQ4) {
+      ptx::mbar_arrive(&sm.q_full);  // Q is in place after the barrier below
+    } else {
+      ptx::mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(n_q * TM * g * D * 2));
+      for (int t = 0; t < n_q; ++t)
+#pragma unroll
+        for (int dh = 0; dh < D / 64; ++dh)  // tokens past the last one read as zeros
+          tma_load_4d(sm.q[t] + dh * (BM * 128), &maps.q, dh * 64, 0, kvh, row.q0 + i0 + t * TM, &sm.q_full);
+    }
+  }
+  if (!POOLQ4 && warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&maps.kb);
+    ptx::prefetch_tmap(&maps.vb);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&sm.tmem_base, kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  if (POOLQ4 && is_softmax && grp < n_q) {
+    // The row's Q in fp16, scaled so that its largest magnitude lies in [2^13, 2^14).
+    const int64_t at = (((int64_t)row.q0 + tok) * a.Hq + kvh * g + trow % g) * D;
+    const uint4* src = reinterpret_cast<const uint4*>((const T*)a.q + at);
+    float top = 0.f;
+    if (valid)
+#pragma unroll 4
+      for (int v = 0; v < D / 8; ++v) {
+        const uint4 x = __ldg(src + v);
+        const T* e = reinterpret_cast<const T*>(&x);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(pkv_to_f32<T>(e[c])));
+      }
+    const int e2 = top > 0.f && top <= 3.402823466e38f ? min(13 - ilogbf(top), 64) : 0;
+    sl2 = scalbnf(sl2, -e2);
+#pragma unroll 4
+    for (int v = 0; v < D / 8; ++v) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (valid) x = __ldg(src + v);
+      const T* e = reinterpret_cast<const T*>(&x);
+      uint32_t w[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        w[c] = ptx::pack_f16x2(scalbnf(pkv_to_f32<T>(e[c]), e2), scalbnf(pkv_to_f32<T>(e[c + 4]), e2));
+      *reinterpret_cast<uint4*>(sm.q[grp] + (v >> 3) * (BM * 128) + trow * 128 + (((v & 7) ^ (trow & 7)) << 4)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    ptx::fence_proxy_async_smem();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+
+  const uint32_t tmem = sm.tmem_base;
+  if (sm.skip) n = 0;
+  constexpr uint32_t O_COL[2] = {256, 256 + D};
+  constexpr uint32_t IDESC_QK = ptx::idesc_f16(BM, BN, OPBF16 ? 1 : 0, 0);
+  constexpr uint32_t IDESC_PV = ptx::idesc_f16(BM, D, OPBF16 ? 1 : 0, 1);
+
+  if (warp < 4) {
+    ptx::regs_dec<kRegsLow>();
+    if (!POOLQ4 && (warp == 0 || warp == 3)) {
+      // ------------------------------------------------------------ producers: warp 0 key tiles, warp 3 value tiles
+      if (warp == 0 && n == 0 && lane == 0) {
+        int never = 0;  // nothing will wait for Q, but its copy must land before the CTA exits
+        ptx::mbar_wait(&sm.q_full, 0, &never, kWaitLimitNs);
+      }
+      for (int idx = warp == 0 ? 0 : 1; idx < 2 * n; idx += 2) {
+        if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) break;
+        const int pos = idx % C::NSLOT, use = idx / C::NSLOT;
+        if (idx >= C::NSLOT && !warp_wait(&sm.empty[pos], (use - 1) & 1, &sm.abort, lane)) {
+          if (lane == 0) note_abort(sm, a.err);
+          break;
+        }
+        load_tile<D>(sm.kv[pos], maps, idx & 1, &sm.full[pos], a, pg, b, kvh, t_begin + (idx >> 1), lane);
+      }
+      if (warp == 0 && *(volatile int*)&sm.abort && lane == 0) {
+        int dummy = 0;  // let copies already issued land before the shared memory goes away
+        ptx::mbar_wait(&sm.q_full, 0, &dummy, kWaitLimitNs);
+      }
+    } else if (POOLQ4 && warp != 1) {
+      // ------------------------------------------------------------ producers of 4-bit tiles
+      // A tile is (BN / 32) x (D / 32) pieces of 32 keys x one group, a lane per key: the eight lanes of a store
+      // phase then write eight rows of one swizzled column, which fall in different banks.  The pieces of a slot
+      // are dealt out in turn, starting with another warp for each slot; the codes of the next slot are loaded
+      // into a piece's registers as soon as they are used up.
+      using F = Q4<D>;
+      constexpr int NPIECE = (BN / 32) * F::kGroups, MINE = (NPIECE + kDequantWarps - 1) / kDequantWarps;
+      const int pw = warp == 0 ? 0 : warp - 1;
+      Q4Piece piece[MINE];
+      int ids = 0, ids_next = 0;  // lane k < 8: block of the tile's page k
+      auto fetch_ids = [&](int j) -> int {
+        const int v = kPages * (t_begin + j) + lane;
+        return j < n && lane < kPages && v < pg.n ? win_block(a, b, pg.page(v)) : 0;
+      };
+      auto load = [&](int idx, int k, int table) {
+        const int wu = (pw + idx) % kDequantWarps + kDequantWarps * k;
+        piece[k].code = make_uint4(0, 0, 0, 0);
+        piece[k].pair = 0;
+        const int rb = wu / F::kGroups, gi = wu % F::kGroups;
+        const int blk = __shfl_sync(0xffffffffu, table, (2 * rb + (lane >> 4)) & (kPages - 1));
+        if (wu >= NPIECE || idx >= 2 * n) return;
+        const int v = kPages * (t_begin + (idx >> 1)) + 2 * rb + (lane >> 4);
+        if (v < pg.n && pg.any(pg.page(v) * 16 + (lane & 15))) {
+          const uint8_t* rec = (const uint8_t*)((idx & 1) ? a.v_pool : a.k_pool) + ((int64_t)blk * a.Hkv + kvh) * F::kRecord;
+          piece[k].code = __ldg(reinterpret_cast<const uint4*>(rec + (lane & 15) * F::kRowBytes + gi * 16));
+          piece[k].pair = __ldg(reinterpret_cast<const uint32_t*>(rec + F::kPairs + ((lane & 15) * F::kGroups + gi) * 4));
+        }
+      };
+      ids = fetch_ids(0);
+#pragma unroll
+      for (int k = 0; k < MINE; ++k) load(0, k, ids);
+      for (int idx = 0; idx < 2 * n; ++idx) {
+        if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) break;
+        if (!(idx & 1)) ids_next = fetch_ids((idx >> 1) + 1);
+        const int pos = idx % C::NSLOT, use = idx / C::NSLOT;
+        if (idx >= C::NSLOT && !warp_wait(&sm.empty[pos], (use - 1) & 1, &sm.abort, lane)) {
+          if (lane == 0) note_abort(sm, a.err);
+          break;
+        }
+        const int table = (idx & 1) ? ids_next : ids;  // the next slot's: V of this tile, or K of the next
+#pragma unroll
+        for (int k = 0; k < MINE; ++k) {
+          const int wu = (pw + idx) % kDequantWarps + kDequantWarps * k;
+          if (wu < NPIECE) {
+            const int r = (wu / F::kGroups) * 32 + lane, gi = wu % F::kGroups;
+            uint8_t* dst = sm.kv[pos] + row_offset<D>(r, gi >> 1);
+            const uint32_t words[4] = {piece[k].code.x, piece[k].code.y, piece[k].code.z, piece[k].code.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              __half2 h[4];
+              q4_values(words[w], *reinterpret_cast<const __half2*>(&piece[k].pair), h);
+              *reinterpret_cast<uint4*>(dst + ((((gi & 1) * 4 + w) ^ (r & 7)) << 4)) =
+                  make_uint4(*reinterpret_cast<uint32_t*>(&h[0]), *reinterpret_cast<uint32_t*>(&h[1]),
+                             *reinterpret_cast<uint32_t*>(&h[2]), *reinterpret_cast<uint32_t*>(&h[3]));
+            }
+          }
+          load(idx + 1, k, table);
+        }
+        if (idx & 1) ids = ids_next;
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.full[pos]);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      if (lane == 0 && n > 0) {
+        const uint32_t kv_base = ptx::smem_u32(sm.kv[0]);
+        bool ok = ptx::mbar_wait(&sm.q_full, 0, &sm.abort, kWaitLimitNs);
+        ptx::tc_fence_after();
+        auto slot_ready = [&](int idx) -> bool {
+          if (!ptx::mbar_wait(&sm.full[idx % C::NSLOT], (idx / C::NSLOT) & 1, &sm.abort, kWaitLimitNs)) return false;
+          ptx::tc_fence_after();
+          return true;
+        };
+        const uint64_t q_desc[2] = {ptx::smem_desc(ptx::smem_u32(sm.q[0]), 16, 1024, 2),
+                                    ptx::smem_desc(ptx::smem_u32(sm.q[1]), 16, 1024, 2)};
+        const uint64_t k_desc = ptx::smem_desc(kv_base, 16, C::GS, 2);
+        const uint64_t v_desc = ptx::smem_desc(kv_base, 1024, C::GS, 2);
+        auto qk = [&](int w, int j) {
+          const uint64_t kd = ptx::desc_add(k_desc, (uint32_t)(((2 * j) % C::NSLOT) * C::TILE) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            ptx::mma_ss(tmem + 128 * w, ptx::desc_add(q_desc[w], ((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4),
+                        ptx::desc_add(kd, ((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), IDESC_QK, ks > 0);
+          ptx::mma_commit(&sm.s_full[w]);
+        };
+        auto pv = [&](int w, int j) {
+          const uint64_t vd = ptx::desc_add(v_desc, (uint32_t)(((2 * j + 1) % C::NSLOT) * C::TILE) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < BN / 16; ++ks)
+            ptx::mma_ts(tmem + O_COL[w], tmem + 128 * w + ks * 8, ptx::desc_add(vd, (ks * 2 * C::GS) >> 4), IDESC_PV,
+                        (j > 0 || ks > 0) ? 1u : 0u);
+        };
+        if (ok) ok = slot_ready(0);
+        if (ok)
+          for (int w = 0; w < n_q; ++w) qk(w, 0);
+        for (int j = 0; ok && j < n; ++j) {
+          const bool next = j + 1 < n;
+          if (!slot_ready(2 * j + 1)) {
+            ok = false;
+            break;
+          }
+          for (int w = 0; w < n_q && ok; ++w) {
+            if (!ptx::mbar_wait(&sm.p_full[w], j & 1, &sm.abort, kWaitLimitNs)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            pv(w, j);
+            if (next) {
+              if (w == 0 && !slot_ready(2 * j + 2)) {
+                ok = false;
+                break;
+              }
+              qk(w, j + 1);
+            }
+          }
+        }
+        if (!ok) note_abort(sm, a.err);
+        ptx::mma_commit(&sm.mma_done);
+        int dummy = 0;
+        ptx::mbar_wait(&sm.mma_done, 0, &dummy, kWaitLimitNs);
+      }
+    }
+  } else {
+    ptx::regs_inc<kRegsHigh>();
+    if (grp < n_q) {
+      // ------------------------------------------------------------ softmax rows of tile grp
+      const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+      const uint32_t S_COL = 128 * grp;
+      const int p = valid ? base + tok : -1;
+      // The warp's rows with queries are consecutive positions [p_lo, p_hi].
+      const int w_first = i0 + grp * TM + (quarter * 32) / g;
+      int w_last = i0 + grp * TM + (quarter * 32 + 31 < TM * g ? quarter * 32 + 31 : TM * g - 1) / g;
+      w_last = w_last < row.Sq ? w_last : row.Sq - 1;
+      const int p_lo = base + w_first, p_hi = base + w_last;
+      float m_ref = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < n; ++j) {
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sm.s_full[grp], j & 1, &sm.abort, kWaitLimitNs))) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        // The last group's scores of tile j are committed after every earlier MMA: key tile j and value tile j-1
+        // are no longer read.
+        if (grp == n_q - 1 && trow == 0) {
+          ptx::mbar_arrive(&sm.empty[(2 * j) % C::NSLOT]);
+          if (j > 0) ptx::mbar_arrive(&sm.empty[(2 * j - 1) % C::NSLOT]);
+        }
+        float s[BN];
+        {
+          uint32_t r[BN / 32][32];
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) ptx::tmem_ld32(tmem + lane_base + S_COL + c * 32, r[c]);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) {
+            ptx::reg_fence32(r[c]);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(r[c][e]);
+          }
+        }
+        // Whole tile seen by all of the warp's rows?  (Pages of a tile ascend.)
+        const int v0 = kPages * (t_begin + j);
+        const int j_first = pg.page(v0) * 16;
+        const int j_last = v0 + kPages <= pg.n ? pg.page(v0 + kPages - 1) * 16 + 15 : 0x7fffffff;
+        if (!(j_last <= p_lo && (a.window == 0 || j_last < a.sinks || p_hi - j_first < a.window))) {
+#pragma unroll
+          for (int k = 0; k < kPages; ++k) {
+            // Column c of the page is seen when c <= hi and (c < sk or c > lo): a 16-bit mask by shifts.
+            unsigned bits = 0;
+            if (v0 + k < pg.n) {
+              const int j0 = pg.page(v0 + k) * 16;
+              const int hi = p - j0, sk = a.sinks - j0, lo = hi - a.window;
+              bits = hi < 0 ? 0u : hi >= 15 ? 0xffffu : (2u << hi) - 1u;
+              if (a.window) {
+                const unsigned head = sk <= 0 ? 0u : sk >= 16 ? 0xffffu : (1u << sk) - 1u;
+                const unsigned tail = lo < 0 ? 0xffffu : lo >= 15 ? 0u : ~((2u << lo) - 1u);
+                bits &= head | tail;
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c) s[k * 16 + c] = (bits >> c) & 1 ? s[k * 16 + c] : -INFINITY;
+          }
+        }
+        float mx[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) mx[u] = fmaxf(s[2 * u], s[2 * u + 1]);
+#pragma unroll
+        for (int c = 16; c < BN; c += 16)
+#pragma unroll
+          for (int u = 0; u < 8; ++u) mx[u] = ptx::max3(mx[u], s[c + 2 * u], s[c + 2 * u + 1]);
+        const float m_tile =
+            fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sl2;
+        const bool need = m_tile > m_ref + kRescale;
+        const bool rescale = __any_sync(0xffffffffu, need);
+        const float alpha = need ? ptx::ex2(m_ref - m_tile) : 1.f;  // 0 on a row's first visible tile
+        if (need) {
+          l *= alpha;
+          m_ref = m_tile;
+        }
+        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+        for (int c = 0; c < BN / 64; ++c) {
+          uint32_t r[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float x0, x1;
+            ptx::fma2(x0, x1, s[c * 64 + 2 * e], s[c * 64 + 2 * e + 1], sl2, sl2, -mu, -mu);
+            const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+            if (e & 1)
+              ptx::add2(l2, l3, p0, p1);
+            else
+              ptx::add2(l0, l1, p0, p1);
+            r[e] = OPBF16 ? ptx::pack_bf16x2(p0, p1) : ptx::pack_f16x2(p0, p1);
+          }
+          ptx::tmem_st32(tmem + lane_base + S_COL + c * 32, r);
+        }
+        l += (l0 + l1) + (l2 + l3);
+        if (rescale && j > 0) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t r[32];
+            ptx::tmem_ld32(tmem + lane_base + O_COL[grp] + c * 32, r);
+            ptx::tmem_wait_ld();
+            ptx::reg_fence32(r);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+            ptx::tmem_st32(tmem + lane_base + O_COL[grp] + c * 32, r);
+          }
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&sm.p_full[grp]);
+      }
+      if (!ok) note_abort(sm, a.err);
+
+      // ---------------------------------------------------------------- epilogue
+      float o[D];
+#pragma unroll
+      for (int c = 0; c < D; ++c) o[c] = 0.f;
+      if (ok && n > 0) {
+        if (__all_sync(0xffffffffu, ptx::mbar_wait(&sm.mma_done, 0, &sm.abort, kWaitLimitNs))) {
+          ptx::tc_fence_after();
+          uint32_t r[D / 32][32];
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) ptx::tmem_ld32(tmem + lane_base + O_COL[grp] + c * 32, r[c]);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            ptx::reg_fence32(r[c]);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              // 4-bit values come in the order of channels (0, 4, 1, 5, 2, 6, 3, 7) of each eight
+              const int ch = POOLQ4 ? (c * 32 + (e & ~7)) + ((e & 1) * 4 + ((e >> 1) & 3)) : c * 32 + e;
+              o[ch] = __uint_as_float(r[c][e]);
+            }
+          }
+        } else {
+          note_abort(sm, a.err);
+          ok = false;
+        }
+      }
+      if (n_cta > 1) {
+        // Staged for the merge in the key/value ring and the Q buffer, which no copy or MMA uses any more.
+        float* st = reinterpret_cast<float*>(sm.kv[0]) + (grp * BM + trow) * C::OSTRIDE;
+#pragma unroll
+        for (int v = 0; v < D / 4; ++v)
+          *reinterpret_cast<float4*>(st + 4 * v) = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+        float* ml = reinterpret_cast<float*>(sm.q[0]);  // [2 BM] maxima, [2 BM] sums
+        ml[grp * BM + trow] = m_ref;
+        ml[2 * BM + grp * BM + trow] = l;
+      } else {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint32_t w[D / 2];
+#pragma unroll
+        for (int c = 0; c < D / 2; ++c) {
+          const float x0 = o[2 * c] * inv, x1 = o[2 * c + 1] * inv;
+          w[c] = OUTBF16 ? ptx::pack_bf16x2(x0, x1) : ptx::pack_f16x2(x0, x1);
+        }
+        // A whole tile leaves through shared memory (the Q buffer, free once every MMA is done) and one TMA store
+        // per column half; a tile with fewer tokens stores per thread.
+        const bool staged = n > 0 && i0 + (grp + 1) * TM <= row.Sq;
+        if (staged) {
+          uint8_t* tile = sm.q[grp];
+#pragma unroll
+          for (int v = 0; v < D / 8; ++v)
+            *reinterpret_cast<uint4*>(tile + (v >> 3) * (BM * 128) + trow * 128 + (((v & 7) ^ (trow & 7)) << 4)) =
+                make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+          ptx::fence_proxy_async_smem();
+          asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(BM) : "memory");
+          if (trow == 0 && !*(volatile int*)&sm.abort) {
+#pragma unroll
+            for (int dh = 0; dh < D / 64; ++dh)
+              tma_store_4d(&maps.o, dh * 64, 0, kvh, row.q0 + i0 + grp * TM, tile + dh * (BM * 128));
+            ptx::bulk_commit();
+            ptx::bulk_wait_read_all();
+          }
+        } else if (valid && ok) {
+          uint4* dst =
+              reinterpret_cast<uint4*>((T*)a.out + (((int64_t)row.q0 + tok) * a.Hq + kvh * g + trow % g) * D);
+#pragma unroll
+          for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+        }
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown, and the cluster's merge
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+  if (n_cta > 1) {
+    __syncwarp();
+    cluster_sync();
+    // Rows r of tile t in turn over the cluster's warps; a lane takes D/32 channels.
+    constexpr int CH = D / 32;
+    const int rows = n_q * BM;
+    for (int e = (int)rank * (kThreads / 32) + warp; e < rows; e += (int)n_cta * (kThreads / 32)) {
+      const int tr = e % BM;
+      const int tk = i0 + (e / BM) * TM + tr / g;
+      if (tr >= TM * g || tk >= row.Sq) continue;
+      float mk = -INFINITY, lk = 0.f;
+      if (lane < (int)n_cta) {
+        const uint32_t ml = cluster_addr(reinterpret_cast<float*>(sm.q[0]) + e, lane);
+        mk = cluster_ld(ml);
+        lk = cluster_ld(ml + 2 * BM * 4);
+      }
+      float top = mk;
+#pragma unroll
+      for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+      const float wk = mk == top ? 1.f : ptx::ex2(mk - top);  // CTAs without keys hold zeros
+      float sum = 0.f, acc[CH] = {};
+      for (int k = 0; k < (int)n_cta; ++k) {
+        const float w = __shfl_sync(0xffffffffu, wk, k);
+        sum += w * __shfl_sync(0xffffffffu, lk, k);
+        const uint32_t src = cluster_addr(reinterpret_cast<float*>(sm.kv[0]) + e * C::OSTRIDE + lane * CH, k);
+#pragma unroll
+        for (int c = 0; c < CH; c += 2) {
+          const float2 x = cluster_ld2(src + c * 4);
+          acc[c] += w * x.x, acc[c + 1] += w * x.y;
+        }
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      T* dst = (T*)a.out + (((int64_t)row.q0 + tk) * a.Hq + kvh * g + tr % g) * D + lane * CH;
+#pragma unroll
+      for (int c = 0; c < CH; c += 2) store_pair<T>(dst + c, acc[c] * inv, acc[c + 1] * inv);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = (EncodeTiledFn)p;
+  });
+  return fn;
+}
+
+bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box, bool bf16) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void*>(base),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, typename T, bool POOLQ4>
+int launch(const PkvWinArgs& a, int64_t Tq, cudaStream_t s) {
+  constexpr bool BF16 = !std::is_same<T, __half>::value;
+  auto kernel = attn_win_tc_kernel<D, T, BF16 && !POOLQ4, POOLQ4>;
+  const int g = a.Hq / a.Hkv, TM = BM / g;
+  WinMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  const cuuint64_t dq[4] = {(cuuint64_t)D, (cuuint64_t)g, (cuuint64_t)a.Hkv, (cuuint64_t)Tq};
+  const cuuint64_t sq[3] = {(cuuint64_t)D * 2, (cuuint64_t)g * D * 2, (cuuint64_t)a.Hq * D * 2};
+  const cuuint32_t bq[4] = {64, (cuuint32_t)g, 1, (cuuint32_t)TM};
+  if (!encode(&maps.o, a.out, 4, dq, sq, bq, BF16)) return (int)cudaErrorInvalidValue;
+  if (!POOLQ4) {
+    const cuuint64_t slots = (cuuint64_t)a.num_blocks * 16, slot = (cuuint64_t)a.Hkv * D * 2;
+    const cuuint64_t d5[5] = {64, 8, (cuuint64_t)(D / 64), slots / 8, (cuuint64_t)a.Hkv};
+    const cuuint64_t s5[4] = {slot, 128, 8 * slot, (cuuint64_t)D * 2};
+    const cuuint32_t b5[5] = {64, 8, (cuuint32_t)(D / 64), 2, 1};
+    const cuuint64_t d3[3] = {(cuuint64_t)D, (cuuint64_t)a.Hkv, slots};
+    const cuuint64_t s3[2] = {(cuuint64_t)D * 2, slot};
+    const cuuint32_t b1[3] = {64, 1, 1};
+    if (!encode(&maps.q, a.q, 4, dq, sq, bq, BF16) || !encode(&maps.kb, a.k_pool, 5, d5, s5, b5, BF16) ||
+        !encode(&maps.vb, a.v_pool, 5, d5, s5, b5, BF16) || !encode(&maps.v1, a.v_pool, 3, d3, s3, b1, BF16))
+      return (int)cudaErrorInvalidValue;
+  }
+  const size_t smem = sizeof(WinSmem<D>) + 1024;
+  static PkvKernelState state;
+  int rc = pkv_prepare_kernel((const void*)kernel, (int)smem, kThreads, kLaunchRegs, state);
+  if (rc) return rc;
+  const int64_t items = (int64_t)a.B * a.Hkv * ((a.max_query_len + 2 * TM - 1) / (2 * TM));
+  const int ctas = pkv_plan_cluster(state, items, pkv_visible_keys(a, 2 * TM) / BN + 1, 4.0);
+  void* args[] = {&maps, const_cast<PkvWinArgs*>(&a)};
+  return pkv_launch_cluster((const void*)kernel, items, ctas, kThreads, smem, args, s);
+}
+
+template <int D, bool POOLQ4>
+int launch_t(const PkvWinArgs& a, int64_t Tq, pkv_dtype dt, cudaStream_t s) {
+  return dt == PKV_BF16 ? launch<D, __nv_bfloat16, POOLQ4>(a, Tq, s) : launch<D, __half, POOLQ4>(a, Tq, s);
+}
+
+}  // namespace
+
+bool pkv_win_tc_supports(const PkvWinArgs& a, pkv_dtype dt) {
+  return (dt == PKV_BF16 || dt == PKV_F16) && a.Hq / a.Hkv <= BM && a.scale > 0.f;
+}
+
+int pkv_launch_win_tc(const PkvWinArgs& a, int64_t Tq, pkv_dtype dt, int D, bool q4, void* stream) {
+  cudaStream_t s = (cudaStream_t)stream;
+  if (q4) return D == 64 ? launch_t<64, true>(a, Tq, dt, s) : launch_t<128, true>(a, Tq, dt, s);
+  return D == 64 ? launch_t<64, false>(a, Tq, dt, s) : launch_t<128, false>(a, Tq, dt, s);
+}

@@ -126,14 +126,23 @@ int pkv_launch_gather_q4(const void* kp, const void* vp, int64_t num_blocks, con
                          int first_block, int n_blocks, void* sk, void* sv, int64_t stage_rows, int Hkv, int D,
                          pkv_dtype dt, unsigned int* err, int check, void* stream);
 int pkv_launch_win_dec(const PkvWinArgs& a, pkv_dtype dt, int D, bool q4, void* stream);
+// tcgen05 path; for calls that pkv_win_tc_supports.
+bool pkv_win_tc_supports(const PkvWinArgs& a, pkv_dtype dt);
+int pkv_launch_win_tc(const PkvWinArgs& a, int64_t Tq, pkv_dtype dt, int D, bool q4, void* stream);
 int pkv_launch_win_simt(const PkvWinArgs& a, pkv_dtype dt, int D, bool q4, void* stream);
 
 // Shared by those launchers (serving.cu).
-// Per-context, once per kernel: opt in to `smem` bytes of dynamic shared memory and to clusters of 16.
-int pkv_prepare_kernel(const void* kernel, int smem, std::atomic<uint64_t> (&done)[64]);
+// Per kernel and device: the context it was prepared in, and how many clusters of 1, 2, 4, 8, 16 CTAs run at once.
+struct PkvKernelState {
+  std::atomic<uint64_t> ctx[64];
+  std::atomic<int> active[64][5];
+};
+// Once per kernel and context: opt in to `smem` bytes of dynamic shared memory and to clusters of 16, read the
+// active clusters; `regs` > 0: refuse a build whose register count is another.
+int pkv_prepare_kernel(const void* kernel, int smem, int threads, int regs, PkvKernelState& state);
 // Keys that a tile of `tokens` query tokens can see, from the sizes the host knows.
 int64_t pkv_visible_keys(const PkvWinArgs& a, int64_t tokens);
-// CTAs (1, 2, 4, 8 or 16) that share one item's `steps` key steps, `per_sm` CTAs being resident on an SM.
-int pkv_plan_cluster(int64_t items, int64_t steps, int per_sm);
-int pkv_launch_cluster(const void* kernel, int64_t items, int ctas, int threads, size_t smem, const PkvWinArgs* a,
+// CTAs (1, 2, 4, 8 or 16) that share one item's `steps` key steps; a CTA's set-up and merge cost about `fixed` steps.
+int pkv_plan_cluster(const PkvKernelState& state, int64_t items, int64_t steps, double fixed);
+int pkv_launch_cluster(const void* kernel, int64_t items, int ctas, int threads, size_t smem, void** args,
                        void* stream);

@@ -103,8 +103,16 @@ pkv_status win_impl(const char* fn, bool q4, const void* q, int64_t Tq, int Hq, 
   a.scale = softmax_scale;
   a.err = pkv_device_error_word();
   if (!a.err) return pkv_fail(PKV_ERR_CUDA, "%s: device error word unavailable", fn);
-  const bool simt = dt == PKV_F32 || (flags & PKV_FORCE_SIMT);
-  const int rc = simt ? pkv_launch_win_simt(a, dt, D, q4, stream) : pkv_launch_win_dec(a, dt, D, q4, stream);
+  // Up to 32 query rows per kv head the memory-bound kernel, which reads each key once for all of them; beyond, tiles
+  // of 256 rows on tcgen05.
+  const int64_t rows = (int64_t)max_query_len * (Hq / Hkv);
+  int rc;
+  if (dt == PKV_F32 || (flags & PKV_FORCE_SIMT))
+    rc = pkv_launch_win_simt(a, dt, D, q4, stream);
+  else if (rows > 32 && num_blocks > 0 && pkv_win_tc_supports(a, dt))
+    rc = pkv_launch_win_tc(a, Tq, dt, D, q4, stream);
+  else
+    rc = pkv_launch_win_dec(a, dt, D, q4, stream);
   if (rc) return pkv_fail(PKV_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString((cudaError_t)rc));
   pkv_set_launches(1);
   return PKV_OK;
@@ -114,17 +122,44 @@ pkv_status win_impl(const char* fn, bool q4, const void* q, int64_t Tq, int Hq, 
 
 // ---------------------------------------------------------------- launches
 
-int pkv_prepare_kernel(const void* kernel, int smem, std::atomic<uint64_t> (&done)[64]) {
-  // Keyed on the context: function attributes belong to the context they were set in.
+int pkv_prepare_kernel(const void* kernel, int smem, int threads, int regs, PkvKernelState& state) {
+  // Keyed on the context: function attributes belong to the context they were set in.  Racing first calls only
+  // repeat the same settings.
   int dev = 0;
   cudaGetDevice(&dev);
-  const bool cached = dev >= 0 && dev < 64;
+  if (dev < 0 || dev >= 64) return (int)cudaErrorInvalidDevice;
   const uint64_t ctx = pkv_context_id();
-  if (cached && ctx != 0 && done[dev].load(std::memory_order_acquire) == ctx) return 0;
+  if (ctx != 0 && state.ctx[dev].load(std::memory_order_acquire) == ctx) return 0;
+  if (regs > 0) {
+    cudaFuncAttributes fa;
+    const cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return (int)e;
+    if (fa.numRegs != regs) return (int)cudaErrorInvalidKernelImage;
+  }
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess && cached) done[dev].store(ctx, std::memory_order_release);
-  return (int)e;
+  if (e != cudaSuccess) return (int)e;
+  for (int i = 0; i < 5; ++i) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1u << i);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << i;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    state.active[dev][i].store(n, std::memory_order_relaxed);
+  }
+  state.ctx[dev].store(ctx, std::memory_order_release);
+  return 0;
 }
 
 int64_t pkv_visible_keys(const PkvWinArgs& a, int64_t tokens) {
@@ -136,24 +171,26 @@ int64_t pkv_visible_keys(const PkvWinArgs& a, int64_t tokens) {
   return keys;
 }
 
-// A launch runs its items' CTAs in waves of (SMs x per_sm); a CTA takes its share of the steps plus a fixed cost
-// (set-up, merge) of about four steps.  The smallest estimate wins; the more CTAs only where they gain a tenth.
-int pkv_plan_cluster(int64_t items, int64_t steps, int per_sm) {
-  int sms = pkv_sm_count();
-  if (sms <= 0) sms = 152;
-  const int64_t slots = (int64_t)sms * per_sm;
+// The launch runs in waves of the clusters that fit the GPU at once; each CTA takes its share of the steps plus the
+// fixed cost.  The smallest estimate wins, a larger cluster only where it gains a tenth.
+int pkv_plan_cluster(const PkvKernelState& state, int64_t items, int64_t steps, double fixed) {
+  int dev = 0;
+  cudaGetDevice(&dev);
   int best = 1;
   double best_cost = 1e300;
-  for (int c = 1; c <= 16; c *= 2) {
+  for (int i = 0; i < 5; ++i) {
+    const int c = 1 << i;
+    const int64_t active = state.active[dev][i].load(std::memory_order_relaxed);
+    if (active <= 0 && c > 1) break;
     if (c > 1 && (steps < 2 * c || items * c > kMaxGrid)) break;
-    const double waves = (double)((items * c + slots - 1) / slots);
-    const double cost = waves * ((double)((steps + c - 1) / c) + 4.0);
+    const int64_t at_once = active > 0 ? active : 152;
+    const double cost = (double)((items + at_once - 1) / at_once) * ((double)((steps + c - 1) / c) + fixed);
     if (cost < 0.9 * best_cost) best = c, best_cost = cost;
   }
   return best;
 }
 
-int pkv_launch_cluster(const void* kernel, int64_t items, int ctas, int threads, size_t smem, const PkvWinArgs* a,
+int pkv_launch_cluster(const void* kernel, int64_t items, int ctas, int threads, size_t smem, void** args,
                        void* stream) {
   if (items * ctas > kMaxGrid) return (int)cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
@@ -168,7 +205,6 @@ int pkv_launch_cluster(const void* kernel, int64_t items, int ctas, int threads,
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  void* args[] = {const_cast<PkvWinArgs*>(a)};
   const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
   const cudaError_t last = cudaGetLastError();
   return (int)(e != cudaSuccess ? e : last);

@@ -413,3 +413,19 @@ def test_repeated_calls_give_the_same_bits(lib, q4):
     a = attention(lib, [(1, 3000), (2, 900)], 8, 2, 128, "bf16", 0, 0, q4, seed=3, poison=False)[0]
     for _ in range(3):
         assert np.array_equal(a, attention(lib, [(1, 3000), (2, 900)], 8, 2, 128, "bf16", 0, 0, q4, seed=3, poison=False)[0])
+
+
+@pytest.mark.parametrize("q4,dtype", [(False, "bf16"), (False, "f16"), (True, "bf16"), (True, "f16")])
+@pytest.mark.parametrize("rows,hq,hkv,d,window,sinks", [
+    ([(300, 300), (0, 40), (257, 900)], 2, 2, 128, 0, 0),       # one head a tile: 128 tokens each
+    ([(300, 700), (129, 129)], 4, 1, 64, 150, 20),
+    ([(77, 1900), (26, 1300)], 5, 1, 128, 400, 130),            # 25 tokens a tile, 125 of its 128 rows
+    ([(50, 5000)], 8, 1, 64, 0, 0),                             # few items over many keys: clusters share them
+    ([(40, 4100), (33, 2050)], 4, 2, 128, 3000, 17),
+    ([(5, 600), (3, 130)], 64, 1, 128, 64, 33),                 # two tokens a tile
+    ([(3, 64), (1, 20)], 128, 1, 64, 0, 0),                     # one token a tile
+    ([(2, 40)], 130, 1, 64, 9, 1),                              # more heads than a tile has rows
+    ([(200, 100), (50, 0)], 2, 1, 128, 30, 2),                  # more queries than keys
+])
+def test_prompt_tiles(lib, rows, hq, hkv, d, window, sinks, dtype, q4):
+    agree(*attention(lib, rows, hq, hkv, d, dtype, window, sinks, q4, seed=hq + len(rows), tail=3))
