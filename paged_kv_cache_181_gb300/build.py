@@ -57,24 +57,30 @@ def _run(cmd: list[str], verbose: bool, log: str | None = None) -> str:
 # bf16/f16 call at run time (the launcher keeps the same check as a backstop).
 TC_SOURCE = "attn_tc.cu"
 TC_KERNEL = "attn_tc_kernel"
-WIN_TC_SOURCE = "attn_win_tc.cu"  # the window/sinks kernel splits its registers the same way
-WIN_TC_KERNEL = "attn_win_tc_kernel"
+# The window/sinks kernel splits its registers the same way; its 4-bit instantiations (last template argument true)
+# have a split of their own.
+WIN_TC_SOURCE = "attn_win_tc.cu"
+REGISTER_GATES = (
+    (TC_SOURCE, TC_KERNEL, "kLaunchRegs"),
+    (WIN_TC_SOURCE, r"attn_win_tc_kernel.*Lb0EEE", "kLaunchRegs"),
+    (WIN_TC_SOURCE, r"attn_win_tc_kernel.*Lb1EEE", "kLaunchRegsQ4"),
+)
 # Sources whose ptxas report is kept beside their object (`<source>.ptxas.txt`): the tensor-core kernel's for
 # the gate below, the CUDA-core kernel's for its spill check (it runs at 252-254 registers, where a
 # toolchain that allocated differently would start spilling: slower, not wrong), and the window kernels' for both.
 PTXAS_LOGGED = (TC_SOURCE, "attn_simt.cu", "attn_win_tc.cu", "attn_win_dec.cu")
 
 
-def expected_tc_registers(source: str) -> int:
-    m = re.search(r"constexpr\s+int\s+kLaunchRegs\s*=\s*(\d+)", source)
+def expected_tc_registers(source: str, name: str = "kLaunchRegs") -> int:
+    m = re.search(rf"constexpr\s+int\s+(?:\w+\s*=\s*\d+\s*,\s*)*{name}\s*=\s*(\d+)", source)
     if not m:
-        raise RuntimeError(f"{TC_SOURCE}: kLaunchRegs not found")
+        raise RuntimeError(f"{name} not found")
     return int(m.group(1))
 
 
 def check_tc_registers(ptxas_log: str, expected: int, kernel: str = TC_KERNEL, source: str = TC_SOURCE) -> int:
-    """Every instantiation of a tensor-core kernel in a ``-Xptxas -v`` log uses ``expected`` registers;
-    returns how many instantiations were checked, raises RuntimeError otherwise."""
+    """Every instantiation of a tensor-core kernel (a regular expression on its mangled name) in a ``-Xptxas -v``
+    log uses ``expected`` registers; returns how many instantiations were checked, raises RuntimeError otherwise."""
     seen = 0
     current = None
     for line in ptxas_log.splitlines():
@@ -84,7 +90,7 @@ def check_tc_registers(ptxas_log: str, expected: int, kernel: str = TC_KERNEL, s
             continue
         m = re.search(r"Used (\d+) registers", line)
         if m and current is not None:
-            if kernel in current:
+            if re.search(kernel, current):
                 seen += 1
                 if int(m.group(1)) != expected:
                     raise RuntimeError(
@@ -151,10 +157,10 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             for f in [ex.submit(_run, cmd, verbose, log) for cmd, log in jobs]:
                 f.result()
-    for source, kernel in ((TC_SOURCE, TC_KERNEL), (WIN_TC_SOURCE, WIN_TC_KERNEL)):
+    for source, kernel, constant in REGISTER_GATES:
         tc_log = os.path.join(OUT_DIR, source + ".ptxas.txt")
         with open(os.path.join(CSRC, source)) as f:
-            expected = expected_tc_registers(f.read())
+            expected = expected_tc_registers(f.read(), constant)
         with open(tc_log) as f:
             log = f.read()
         try:

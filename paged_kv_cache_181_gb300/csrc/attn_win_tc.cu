@@ -14,8 +14,8 @@
 //
 // Warps: 1 issues the MMAs and owns TMEM; 4-7 and 8-11 are the softmax of the two tiles, one row per thread; and
 //   16-bit pools: 0 loads Q and the key tiles by TMA (one box per page), 3 the value tiles;
-//   4-bit pools:  0, 2 and 3 read codes, turn them into the fp16 numbers they stand for and store them swizzled as
-//                 TMA would; Q is converted to fp16 by the softmax threads, each row scaled by a power of two.
+//   4-bit pools:  0 copies whole records to shared memory, 2, 3 and 12-15 turn their codes into the fp16 numbers they
+//                 stand for and store them swizzled as TMA would; Q is converted to fp16 by the softmax threads, each row scaled by a power of two.
 //                 Channels of a code word come out as (0,4), (1,5), (2,6), (3,7): Q's and the output's channels are
 //                 permuted to match, which is free, instead of the codes.
 // The order of MMAs, the ring of slots shared by key and value tiles, the lazy rescale and the register split between
@@ -38,35 +38,47 @@ namespace {
 constexpr int BM = 128;  // rows per tile; two tiles per CTA
 constexpr int BN = 128;  // keys per tile
 constexpr int kPages = BN / 16;
-constexpr int kThreads = 384;
-constexpr int kLaunchRegs = 168;  // registers per thread the kernel is compiled to (checked at launch)
-constexpr int kRegsLow = 104, kRegsHigh = 200;
-static_assert(128 * kRegsLow + 256 * kRegsHigh == kThreads * kLaunchRegs, "register split must add up");
+// Threads, and registers per thread: as compiled (checked at build and launch), and after the split between the
+// producer/MMA warpgroups and the two softmax ones.
+constexpr int kLaunchRegs = 168, kLaunchRegsQ4 = 128;
+template <bool POOLQ4>
+struct Roles {
+  static constexpr int kThreads = POOLQ4 ? 512 : 384;
+  static constexpr int kRegs = POOLQ4 ? kLaunchRegsQ4 : kLaunchRegs;
+  static constexpr int kLow = POOLQ4 ? 72 : 104, kHigh = POOLQ4 ? 184 : 200;
+  static_assert((kThreads - 256) * kLow + 256 * kHigh == kThreads * kRegs, "register split must add up");
+};
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kRescale = 8.f;  // log2 units
-constexpr int kDequantWarps = 3;
+constexpr int kDequantWarps = 6;
 
-template <int D>
+template <int D, bool POOLQ4>
 struct Cfg {
   static constexpr int TILE = BN * D * 2;
-  static constexpr int NSLOT = D == 128 ? 5 : 10;
+  static constexpr int NSLOT = (POOLQ4 ? 4 : 5) * (128 / D);
+  static constexpr int NRAW = POOLQ4 ? 3 : 0;             // 4-bit tiles in flight
+  static constexpr int RAW = kPages * Q4<D>::kRecord;     // one of them
   static constexpr int GS = (D / 64) * 1024;  // stride of 8-row atoms in a key/value tile
   static constexpr int OSTRIDE = D + 4;       // floats between rows staged for the merge
 };
 
-template <int D>
+template <int D, bool POOLQ4>
 struct alignas(1024) WinSmem {
-  uint8_t q[2][BM * D * 2];                 // [D/64][128 rows][128 B] per tile, 128-byte swizzled
-  uint8_t kv[Cfg<D>::NSLOT][Cfg<D>::TILE];  // [page][8-row group][column half][8 rows][128 B], swizzled
-  uint64_t full[Cfg<D>::NSLOT], empty[Cfg<D>::NSLOT];
+  using C = Cfg<D, POOLQ4>;
+  uint8_t q[2][BM * D * 2];       // [D/64][128 rows][128 B] per tile, 128-byte swizzled
+  uint8_t kv[C::NSLOT][C::TILE];  // [page][8-row group][column half][8 rows][128 B], swizzled
+  uint8_t raw[POOLQ4 ? C::NRAW : 1][POOLQ4 ? C::RAW : 16];  // records of 4-bit tiles
+  uint64_t full[C::NSLOT], empty[C::NSLOT];
+  uint64_t raw_full[3], raw_empty[3];
   uint64_t q_full, s_full[2], p_full[2], mma_done;
   uint32_t tmem_base;
   int abort, skip;
+  // The merge stages 2 BM rows of OSTRIDE floats from kv on.
+  static_assert(2 * BM * C::OSTRIDE * 4 <= C::NSLOT * C::TILE + C::NRAW * C::RAW, "merge rows fit");
 };
-static_assert(sizeof(WinSmem<128>) + 1024 <= 227 * 1024, "shared memory of a CTA");
-static_assert(2 * BM * Cfg<128>::OSTRIDE * 4 <= sizeof(WinSmem<128>::kv), "merge rows fit the ring");
-static_assert(2 * BM * Cfg<64>::OSTRIDE * 4 <= sizeof(WinSmem<64>::kv), "merge rows fit the ring");
+static_assert(sizeof(WinSmem<128, false>) + 1024 <= 227 * 1024 && sizeof(WinSmem<128, true>) + 1024 <= 227 * 1024,
+              "shared memory of a CTA");
 
 struct WinMaps {
   CUtensorMap q, o;    // (D, g, Hkv, Tq), box = 64 columns x g heads x a tile's tokens
@@ -76,7 +88,7 @@ struct WinMaps {
 
 template <int D>
 __host__ __device__ constexpr int row_offset(int r, int dh) {
-  return (r >> 4) * (2 * Cfg<D>::GS) + ((r >> 3) & 1) * Cfg<D>::GS + dh * 1024 + (r & 7) * 128;
+  return (r >> 3) * ((D / 64) * 1024) + dh * 1024 + (r & 7) * 128;
 }
 
 PKV_DEVINLINE void tma_load_4d(void* dst, const void* tmap, int c0, int c1, int c2, int c3, uint64_t* bar) {
@@ -92,8 +104,16 @@ PKV_DEVINLINE void tma_store_4d(const void* tmap, int c0, int c1, int c2, int c3
                : "memory");
 }
 
-template <int D>
-PKV_DEVINLINE void note_abort(WinSmem<D>& sm, unsigned int* err) {
+// Bytes [src, src + n) of global memory to shared memory, counted on `bar`; all multiples of 16.
+PKV_DEVINLINE void bulk_load(void* dst, const void* src, uint32_t n, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   ptx::smem_u32(dst)),
+               "l"(src), "r"(n), "r"(ptx::smem_u32(bar))
+               : "memory");
+}
+
+template <typename Smem>
+PKV_DEVINLINE void note_abort(Smem& sm, unsigned int* err) {
   sm.abort = 1;
   pkv_raise(err, PKV_DEVERR_TIMEOUT);
 }
@@ -148,19 +168,15 @@ PKV_DEVINLINE void load_tile(uint8_t* dst, const WinMaps& maps, bool is_v, uint6
   }
 }
 
-// A lane's piece of a 4-bit tile: 32 channels (one group) of one key.
-struct Q4Piece {
-  uint4 code;
-  uint32_t pair;
-};
-
 template <int D, typename T, bool OPBF16, bool POOLQ4>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
     attn_win_tc_kernel(const __grid_constant__ WinMaps maps, const PkvWinArgs a) {
-  using C = Cfg<D>;
+  using C = Cfg<D, POOLQ4>;
+  constexpr int kThreads = Roles<POOLQ4>::kThreads;
   constexpr bool OUTBF16 = !std::is_same<T, __half>::value;
   extern __shared__ uint8_t smem_raw[];
-  WinSmem<D>& sm = *reinterpret_cast<WinSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  using Smem = WinSmem<D, POOLQ4>;
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.Hq / a.Hkv;
   const int TM = BM / g;  // tokens per tile
@@ -185,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int n = t_end > t_begin ? t_end - t_begin : 0;
 
   const int grp = warp >= 8 ? 1 : 0;
-  const bool is_softmax = warp >= 4;
+  const bool is_softmax = warp >= 4 && warp < 12;
   const int quarter = warp & 3;
   const int trow = quarter * 32 + lane;             // row of the tile
   const int tok = i0 + grp * TM + trow / g;         // local query token of the row
@@ -196,6 +212,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < C::NSLOT; ++s) {
       ptx::mbar_init(&sm.full[s], POOLQ4 ? kDequantWarps : 1);
       ptx::mbar_init(&sm.empty[s], 1);
+    }
+    for (int s = 0; s < 3; ++s) {
+      ptx::mbar_init(&sm.raw_full[s], 1);
+      ptx::mbar_init(&sm.raw_empty[s], kDequantWarps);
     }
     ptx::mbar_init(&sm.q_full, 1);
     for (int w = 0; w < 2; ++w) {
@@ -264,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t IDESC_QK = ptx::idesc_f16(BM, BN, OPBF16 ? 1 : 0, 0);
   constexpr uint32_t IDESC_PV = ptx::idesc_f16(BM, D, OPBF16 ? 1 : 0, 1);
 
-  if (warp < 4) {
-    ptx::regs_dec<kRegsLow>();
+  if (!is_softmax) {
+    ptx::regs_dec<Roles<POOLQ4>::kLow>();
     if (!POOLQ4 && (warp == 0 || warp == 3)) {
       // ------------------------------------------------------------ producers: warp 0 key tiles, warp 3 value tiles
       if (warp == 0 && n == 0 && lane == 0) {
@@ -285,69 +305,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         int dummy = 0;  // let copies already issued land before the shared memory goes away
         ptx::mbar_wait(&sm.q_full, 0, &dummy, kWaitLimitNs);
       }
-    } else if (POOLQ4 && warp != 1) {
-      // ------------------------------------------------------------ producers of 4-bit tiles
-      // A tile is (BN / 32) x (D / 32) pieces of 32 keys x one group, a lane per key: the eight lanes of a store
-      // phase then write eight rows of one swizzled column, which fall in different banks.  The pieces of a slot
-      // are dealt out in turn, starting with another warp for each slot; the codes of the next slot are loaded
-      // into a piece's registers as soon as they are used up.
-      using F = Q4<D>;
-      constexpr int NPIECE = (BN / 32) * F::kGroups, MINE = (NPIECE + kDequantWarps - 1) / kDequantWarps;
-      const int pw = warp == 0 ? 0 : warp - 1;
-      Q4Piece piece[MINE];
-      int ids = 0, ids_next = 0;  // lane k < 8: block of the tile's page k
-      auto fetch_ids = [&](int j) -> int {
-        const int v = kPages * (t_begin + j) + lane;
-        return j < n && lane < kPages && v < pg.n ? win_block(a, b, pg.page(v)) : 0;
-      };
-      auto load = [&](int idx, int k, int table) {
-        const int wu = (pw + idx) % kDequantWarps + kDequantWarps * k;
-        piece[k].code = make_uint4(0, 0, 0, 0);
-        piece[k].pair = 0;
-        const int rb = wu / F::kGroups, gi = wu % F::kGroups;
-        const int blk = __shfl_sync(0xffffffffu, table, (2 * rb + (lane >> 4)) & (kPages - 1));
-        if (wu >= NPIECE || idx >= 2 * n) return;
-        const int v = kPages * (t_begin + (idx >> 1)) + 2 * rb + (lane >> 4);
-        if (v < pg.n && pg.any(pg.page(v) * 16 + (lane & 15))) {
-          const uint8_t* rec = (const uint8_t*)((idx & 1) ? a.v_pool : a.k_pool) + ((int64_t)blk * a.Hkv + kvh) * F::kRecord;
-          piece[k].code = __ldg(reinterpret_cast<const uint4*>(rec + (lane & 15) * F::kRowBytes + gi * 16));
-          piece[k].pair = __ldg(reinterpret_cast<const uint32_t*>(rec + F::kPairs + ((lane & 15) * F::kGroups + gi) * 4));
-        }
-      };
-      ids = fetch_ids(0);
-#pragma unroll
-      for (int k = 0; k < MINE; ++k) load(0, k, ids);
+    } else if (POOLQ4 && warp == 0) {
+      // ------------------------------------------------------------ 4-bit tiles: a lane per page copies its record
+      int ids = 0;
       for (int idx = 0; idx < 2 * n; ++idx) {
         if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) break;
-        if (!(idx & 1)) ids_next = fetch_ids((idx >> 1) + 1);
-        const int pos = idx % C::NSLOT, use = idx / C::NSLOT;
-        if (idx >= C::NSLOT && !warp_wait(&sm.empty[pos], (use - 1) & 1, &sm.abort, lane)) {
+        const int v = kPages * (t_begin + (idx >> 1)) + lane;
+        const bool there = lane < kPages && v < pg.n;
+        if (!(idx & 1) && there) ids = win_block(a, b, pg.page(v));
+        const int pos = idx % 3, use = idx / 3;
+        if (use > 0 && !warp_wait(&sm.raw_empty[pos], (use - 1) & 1, &sm.abort, lane)) {
           if (lane == 0) note_abort(sm, a.err);
           break;
         }
-        const int table = (idx & 1) ? ids_next : ids;  // the next slot's: V of this tile, or K of the next
-#pragma unroll
-        for (int k = 0; k < MINE; ++k) {
-          const int wu = (pw + idx) % kDequantWarps + kDequantWarps * k;
-          if (wu < NPIECE) {
-            const int r = (wu / F::kGroups) * 32 + lane, gi = wu % F::kGroups;
-            uint8_t* dst = sm.kv[pos] + row_offset<D>(r, gi >> 1);
-            const uint32_t words[4] = {piece[k].code.x, piece[k].code.y, piece[k].code.z, piece[k].code.w};
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              __half2 h[4];
-              q4_values(words[w], *reinterpret_cast<const __half2*>(&piece[k].pair), h);
-              *reinterpret_cast<uint4*>(dst + ((((gi & 1) * 4 + w) ^ (r & 7)) << 4)) =
-                  make_uint4(*reinterpret_cast<uint32_t*>(&h[0]), *reinterpret_cast<uint32_t*>(&h[1]),
-                             *reinterpret_cast<uint32_t*>(&h[2]), *reinterpret_cast<uint32_t*>(&h[3]));
-            }
-          }
-          load(idx + 1, k, table);
+        const int pages = __popc(__ballot_sync(0xffffffffu, there));
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&sm.raw_full[pos], (uint32_t)(pages * Q4<D>::kRecord));
+        __syncwarp();
+        if (there)
+          bulk_load(sm.raw[POOLQ4 ? pos : 0] + lane * Q4<D>::kRecord,
+                    (const uint8_t*)((idx & 1) ? a.v_pool : a.k_pool) + ((int64_t)ids * a.Hkv + kvh) * Q4<D>::kRecord,
+                    Q4<D>::kRecord, &sm.raw_full[pos]);
+      }
+      if (*(volatile int*)&sm.abort && lane == 0) {
+        // Let copies already issued land before the shared memory goes away.
+        int never = 0;
+        for (int s = 0; s < 3; ++s) ptx::mbar_wait(&sm.raw_full[s], 0, &never, 1000000ull);
+      }
+    } else if (POOLQ4 && warp != 1) {
+      // ------------------------------------------------------------ 4-bit tiles: codes to fp16, swizzled as TMA would
+      // A lane takes one group of 32 channels of one key: 16 bytes of codes in, four 16-byte chunks out.  A warp's
+      // piece is 32 / (D/32) keys of all groups, so its reads are contiguous; which of the four chunks a lane stores
+      // first depends on its key and group such that the eight lanes of a store phase hit different banks.  The
+      // pieces of a slot are dealt out in turn, starting with another warp for each slot.
+      using F = Q4<D>;
+      constexpr int G = F::kGroups, KEYS = 32 / G, NPIECE = BN / KEYS;
+      const int pw = warp < 4 ? warp - 2 : warp - 10;
+      const int gi = lane % G, rk = lane / G;
+      const int x = D == 128 ? (gi >> 1) | ((rk & 1) << 1) : 0;  // chunk order: 0^x, 1^x, 2^x, 3^x
+      for (int idx = 0; idx < 2 * n; ++idx) {
+        if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) break;
+        const int pos = idx % C::NSLOT, use = idx / C::NSLOT, rpos = idx % 3;
+        if (!warp_wait(&sm.raw_full[rpos], (idx / 3) & 1, &sm.abort, lane) ||
+            (use > 0 && !warp_wait(&sm.empty[pos], (use - 1) & 1, &sm.abort, lane))) {
+          if (lane == 0) note_abort(sm, a.err);
+          break;
         }
-        if (idx & 1) ids = ids_next;
+        const uint8_t* raw = sm.raw[POOLQ4 ? rpos : 0];
+        for (int piece = (pw + idx) % kDequantWarps; piece < NPIECE; piece += kDequantWarps) {
+          const int r = piece * KEYS + rk;  // key of the tile
+          const int v = kPages * (t_begin + (idx >> 1)) + (r >> 4);
+          uint4 code = make_uint4(0, 0, 0, 0);
+          uint32_t pair = 0;  // keys that no row sees are zeros
+          if (v < pg.n && pg.any(pg.page(v) * 16 + (r & 15))) {
+            const uint8_t* rec = raw + (r >> 4) * F::kRecord;
+            code = *reinterpret_cast<const uint4*>(rec + (r & 15) * F::kRowBytes + gi * 16);
+            pair = *reinterpret_cast<const uint32_t*>(rec + F::kPairs + ((r & 15) * G + gi) * 4);
+          }
+          const uint32_t y0 = (x & 1) ? code.y : code.x, y1 = (x & 1) ? code.x : code.y;
+          const uint32_t y2 = (x & 1) ? code.w : code.z, y3 = (x & 1) ? code.z : code.w;
+          const uint32_t words[4] = {(x & 2) ? y2 : y0, (x & 2) ? y3 : y1, (x & 2) ? y0 : y2, (x & 2) ? y1 : y3};
+          uint8_t* dst = sm.kv[pos] + row_offset<D>(r, gi >> 1);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            __half2 h[4];
+            q4_values(words[w], *reinterpret_cast<const __half2*>(&pair), h);
+            *reinterpret_cast<uint4*>(dst + ((((gi & 1) * 4 + (w ^ x)) ^ (r & 7)) << 4)) =
+                make_uint4(*reinterpret_cast<uint32_t*>(&h[0]), *reinterpret_cast<uint32_t*>(&h[1]),
+                           *reinterpret_cast<uint32_t*>(&h[2]), *reinterpret_cast<uint32_t*>(&h[3]));
+          }
+        }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sm.full[pos]);
+        if (lane == 0) {
+          ptx::mbar_arrive(&sm.full[pos]);
+          ptx::mbar_arrive(&sm.raw_empty[rpos]);
+        }
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
@@ -411,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    ptx::regs_inc<kRegsHigh>();
+    ptx::regs_inc<Roles<POOLQ4>::kHigh>();
     if (grp < n_q) {
       // ------------------------------------------------------------ softmax rows of tile grp
       const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -696,14 +728,14 @@ int launch(const PkvWinArgs& a, int64_t Tq, cudaStream_t s) {
         !encode(&maps.vb, a.v_pool, 5, d5, s5, b5, BF16) || !encode(&maps.v1, a.v_pool, 3, d3, s3, b1, BF16))
       return (int)cudaErrorInvalidValue;
   }
-  const size_t smem = sizeof(WinSmem<D>) + 1024;
+  const size_t smem = sizeof(WinSmem<D, POOLQ4>) + 1024;
   static PkvKernelState state;
-  int rc = pkv_prepare_kernel((const void*)kernel, (int)smem, kThreads, kLaunchRegs, state);
+  int rc = pkv_prepare_kernel((const void*)kernel, (int)smem, Roles<POOLQ4>::kThreads, Roles<POOLQ4>::kRegs, state);
   if (rc) return rc;
   const int64_t items = (int64_t)a.B * a.Hkv * ((a.max_query_len + 2 * TM - 1) / (2 * TM));
   const int ctas = pkv_plan_cluster(state, items, pkv_visible_keys(a, 2 * TM) / BN + 1, 4.0);
   void* args[] = {&maps, const_cast<PkvWinArgs*>(&a)};
-  return pkv_launch_cluster((const void*)kernel, items, ctas, kThreads, smem, args, s);
+  return pkv_launch_cluster((const void*)kernel, items, ctas, Roles<POOLQ4>::kThreads, smem, args, s);
 }
 
 template <int D, bool POOLQ4>
