@@ -314,7 +314,8 @@ PKV_API pkv_status paged_kv_gather_q4(const void* key_pool, const void* value_po
  * Table entries of blocks that no query of the row sees are not read: evicted blocks may hold any id.  Keys and
  * values that no query of the row sees do not enter any output, whatever they hold; a NaN or an infinity in a
  * value that some query of the row sees may also reach the row's other queries.
- * One launch, no workspace: CTAs that share a query tile's keys form a cluster and merge through its shared memory.
+ * No workspace: CTAs that share a query tile's keys form a cluster and merge through its shared memory.  One launch,
+ * or two where a prompt's query tiles leave a last wave partly filled (the second splits that wave's tiles).
  * Out rows past query_start_loc[B] are left as they are.
  *   window, sinks  >= 0
  *   softmax_scale  finite; > 0 for bf16/f16 unless flags holds PKV_FORCE_SIMT

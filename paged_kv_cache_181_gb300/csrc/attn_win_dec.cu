@@ -485,7 +485,7 @@ int launch(const PkvWinArgs& a, cudaStream_t s) {
   const int64_t items = (int64_t)a.B * a.Hkv * (((int64_t)a.max_query_len * g + 8 * NT - 1) / (8 * NT));
   const int ctas = pkv_plan_cluster(state, items, pkv_visible_keys(a, 8 * NT / g + 1) / (16 * kWarps) + 1, 4.0);
   void* args[] = {const_cast<PkvWinArgs*>(&a)};
-  return pkv_launch_cluster((const void*)kernel, items, ctas, kThreads, smem, args, s);
+  return pkv_launch_cluster((const void*)kernel, items, ctas, kThreads, smem, args, false, s);
 }
 
 template <typename T, bool POOLQ4, int D>

@@ -182,7 +182,7 @@ int launch(const PkvWinArgs& a, cudaStream_t s) {
   const int64_t items = (int64_t)a.B * a.Hkv * (((int64_t)a.max_query_len * g + kRows - 1) / kRows);
   const int ctas = pkv_plan_cluster(state, items, pkv_visible_keys(a, kRows / g + 1) / kKeys + 1, 2.0);
   void* args[] = {const_cast<PkvWinArgs*>(&a)};
-  return pkv_launch_cluster((const void*)kernel, items, ctas, kThreads, smem, args, s);
+  return pkv_launch_cluster((const void*)kernel, items, ctas, kThreads, smem, args, false, s);
 }
 
 template <typename T, typename Pool>

@@ -52,6 +52,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr float kRescale = 8.f;  // log2 units
 constexpr int kDequantWarps = 6;
+constexpr double kFixedTiles = 4.0;  // a CTA's set-up and epilogue, in key tiles of its time
 
 template <int D, bool POOLQ4>
 struct Cfg {
@@ -170,7 +171,7 @@ PKV_DEVINLINE void load_tile(uint8_t* dst, const WinMaps& maps, bool is_v, uint6
 
 template <int D, typename T, bool OPBF16, bool POOLQ4>
 __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
-    attn_win_tc_kernel(const __grid_constant__ WinMaps maps, const PkvWinArgs a) {
+    attn_win_tc_kernel(const __grid_constant__ WinMaps maps, const PkvWinArgs a, const uint32_t first_item) {
   using C = Cfg<D, POOLQ4>;
   constexpr int kThreads = Roles<POOLQ4>::kThreads;
   constexpr bool OUTBF16 = !std::is_same<T, __half>::value;
@@ -182,14 +183,19 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
   const int TM = BM / g;  // tokens per tile
   const uint32_t rank = cluster_rank(), n_cta = cluster_size();
   // Items with the latest queries (the most keys) first; the kv heads of one stretch of queries run together.
-  uint32_t item = blockIdx.x / n_cta;
+  uint32_t item = first_item + blockIdx.x / n_cta;
+  // A second launch, for the items behind whole waves, may start as soon as this one's last CTAs run.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int n_qp = (a.max_query_len + 2 * TM - 1) / (2 * TM);
   const int kvh = item % a.Hkv;
   item /= a.Hkv;
   const int b = item % a.B, qp = n_qp - 1 - item / a.B;
   const WinRow row = win_row(a, b, tid == 0 && qp == 0 && kvh == 0 && rank == 0);
   const int i0 = qp * 2 * TM;
-  if (i0 >= row.Sq) return;  // the whole cluster leaves
+  if (i0 >= row.Sq) {  // the whole cluster leaves
+    if (first_item) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int n_q = i0 + TM < row.Sq ? 2 : 1;
   const int base = row.L - row.Sq;
   const int last = row.Sq < i0 + 2 * TM ? row.Sq : i0 + 2 * TM;  // one past the CTA's last token
@@ -338,37 +344,53 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
       // first depends on its key and group such that the eight lanes of a store phase hit different banks.  The
       // pieces of a slot are dealt out in turn, starting with another warp for each slot.
       using F = Q4<D>;
-      constexpr int G = F::kGroups, KEYS = 32 / G, NPIECE = BN / KEYS;
+      constexpr int G = F::kGroups, KEYS = 32 / G;
+      constexpr int MINE = (BN / KEYS + kDequantWarps - 1) / kDequantWarps;
       const int pw = warp < 4 ? warp - 2 : warp - 10;
       const int gi = lane % G, rk = lane / G;
       const int x = D == 128 ? (gi >> 1) | ((rk & 1) << 1) : 0;  // chunk order: 0^x, 1^x, 2^x, 3^x
       for (int idx = 0; idx < 2 * n; ++idx) {
         if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) break;
         const int pos = idx % C::NSLOT, use = idx / C::NSLOT, rpos = idx % 3;
-        if (!warp_wait(&sm.raw_full[rpos], (idx / 3) & 1, &sm.abort, lane) ||
-            (use > 0 && !warp_wait(&sm.empty[pos], (use - 1) & 1, &sm.abort, lane))) {
+        if (!warp_wait(&sm.raw_full[rpos], (idx / 3) & 1, &sm.abort, lane)) {
           if (lane == 0) note_abort(sm, a.err);
           break;
         }
+        // All of the warp's codes first: the reads overlap each other and the wait for the slot.
         const uint8_t* raw = sm.raw[POOLQ4 ? rpos : 0];
-        for (int piece = (pw + idx) % kDequantWarps; piece < NPIECE; piece += kDequantWarps) {
-          const int r = piece * KEYS + rk;  // key of the tile
+        const int p0 = (pw + idx) % kDequantWarps;
+        uint4 code[MINE];
+        uint32_t pair[MINE];
+#pragma unroll
+        for (int k = 0; k < MINE; ++k) {
+          const int r = (p0 + k * kDequantWarps) * KEYS + rk;  // key of the tile
           const int v = kPages * (t_begin + (idx >> 1)) + (r >> 4);
-          uint4 code = make_uint4(0, 0, 0, 0);
-          uint32_t pair = 0;  // keys that no row sees are zeros
-          if (v < pg.n && pg.any(pg.page(v) * 16 + (r & 15))) {
+          code[k] = make_uint4(0, 0, 0, 0);
+          pair[k] = 0;  // keys that no row sees are zeros
+          if (r < BN && v < pg.n && pg.any(pg.page(v) * 16 + (r & 15))) {
             const uint8_t* rec = raw + (r >> 4) * F::kRecord;
-            code = *reinterpret_cast<const uint4*>(rec + (r & 15) * F::kRowBytes + gi * 16);
-            pair = *reinterpret_cast<const uint32_t*>(rec + F::kPairs + ((r & 15) * G + gi) * 4);
+            code[k] = *reinterpret_cast<const uint4*>(rec + (r & 15) * F::kRowBytes + gi * 16);
+            pair[k] = *reinterpret_cast<const uint32_t*>(rec + F::kPairs + ((r & 15) * G + gi) * 4);
           }
-          const uint32_t y0 = (x & 1) ? code.y : code.x, y1 = (x & 1) ? code.x : code.y;
-          const uint32_t y2 = (x & 1) ? code.w : code.z, y3 = (x & 1) ? code.z : code.w;
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.raw_empty[rpos]);
+        if (use > 0 && !warp_wait(&sm.empty[pos], (use - 1) & 1, &sm.abort, lane)) {
+          if (lane == 0) note_abort(sm, a.err);
+          break;
+        }
+#pragma unroll
+        for (int k = 0; k < MINE; ++k) {
+          const int r = (p0 + k * kDequantWarps) * KEYS + rk;
+          if (r >= BN) break;
+          const uint32_t y0 = (x & 1) ? code[k].y : code[k].x, y1 = (x & 1) ? code[k].x : code[k].y;
+          const uint32_t y2 = (x & 1) ? code[k].w : code[k].z, y3 = (x & 1) ? code[k].z : code[k].w;
           const uint32_t words[4] = {(x & 2) ? y2 : y0, (x & 2) ? y3 : y1, (x & 2) ? y0 : y2, (x & 2) ? y1 : y3};
           uint8_t* dst = sm.kv[pos] + row_offset<D>(r, gi >> 1);
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             __half2 h[4];
-            q4_values(words[w], *reinterpret_cast<const __half2*>(&pair), h);
+            q4_values(words[w], *reinterpret_cast<const __half2*>(&pair[k]), h);
             *reinterpret_cast<uint4*>(dst + ((((gi & 1) * 4 + (w ^ x)) ^ (r & 7)) << 4)) =
                 make_uint4(*reinterpret_cast<uint32_t*>(&h[0]), *reinterpret_cast<uint32_t*>(&h[1]),
                            *reinterpret_cast<uint32_t*>(&h[2]), *reinterpret_cast<uint32_t*>(&h[3]));
@@ -376,10 +398,7 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(&sm.full[pos]);
-          ptx::mbar_arrive(&sm.raw_empty[rpos]);
-        }
+        if (lane == 0) ptx::mbar_arrive(&sm.full[pos]);
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
@@ -674,6 +693,8 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
     __syncwarp();
     cluster_sync();
   }
+  // A second launch completes after the first: what follows on the stream waits for it alone.
+  if (first_item) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- host side
@@ -706,7 +727,7 @@ bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, 
 }
 
 template <int D, typename T, bool POOLQ4>
-int launch(const PkvWinArgs& a, int64_t Tq, cudaStream_t s) {
+int launch(const PkvWinArgs& a, int64_t Tq, int* launches, cudaStream_t s) {
   constexpr bool BF16 = !std::is_same<T, __half>::value;
   auto kernel = attn_win_tc_kernel<D, T, BF16 && !POOLQ4, POOLQ4>;
   const int g = a.Hq / a.Hkv, TM = BM / g;
@@ -733,14 +754,30 @@ int launch(const PkvWinArgs& a, int64_t Tq, cudaStream_t s) {
   int rc = pkv_prepare_kernel((const void*)kernel, (int)smem, Roles<POOLQ4>::kThreads, Roles<POOLQ4>::kRegs, state);
   if (rc) return rc;
   const int64_t items = (int64_t)a.B * a.Hkv * ((a.max_query_len + 2 * TM - 1) / (2 * TM));
-  const int ctas = pkv_plan_cluster(state, items, pkv_visible_keys(a, 2 * TM) / BN + 1, 4.0);
-  void* args[] = {&maps, const_cast<PkvWinArgs*>(&a)};
-  return pkv_launch_cluster((const void*)kernel, items, ctas, Roles<POOLQ4>::kThreads, smem, args, s);
+  const int64_t steps = pkv_visible_keys(a, 2 * TM) / BN + 1;
+  const PkvClusterPlan plan = pkv_plan_cluster_tail(state, items, steps, kFixedTiles);
+  uint32_t first = 0;
+  void* args[] = {&maps, const_cast<PkvWinArgs*>(&a), &first};
+  *launches = 0;
+  if (plan.whole > 0) {
+    rc = pkv_launch_cluster((const void*)kernel, plan.whole, 1, Roles<POOLQ4>::kThreads, smem, args, false, s);
+    if (rc) return rc;
+    ++*launches;
+    first = (uint32_t)plan.whole;
+  }
+  if (items > plan.whole) {
+    rc = pkv_launch_cluster((const void*)kernel, items - plan.whole, plan.ctas, Roles<POOLQ4>::kThreads, smem, args,
+                            first != 0, s);
+    if (rc) return rc;
+    ++*launches;
+  }
+  return 0;
 }
 
 template <int D, bool POOLQ4>
-int launch_t(const PkvWinArgs& a, int64_t Tq, pkv_dtype dt, cudaStream_t s) {
-  return dt == PKV_BF16 ? launch<D, __nv_bfloat16, POOLQ4>(a, Tq, s) : launch<D, __half, POOLQ4>(a, Tq, s);
+int launch_t(const PkvWinArgs& a, int64_t Tq, pkv_dtype dt, int* launches, cudaStream_t s) {
+  return dt == PKV_BF16 ? launch<D, __nv_bfloat16, POOLQ4>(a, Tq, launches, s)
+                        : launch<D, __half, POOLQ4>(a, Tq, launches, s);
 }
 
 }  // namespace
@@ -749,8 +786,8 @@ bool pkv_win_tc_supports(const PkvWinArgs& a, pkv_dtype dt) {
   return (dt == PKV_BF16 || dt == PKV_F16) && a.Hq / a.Hkv <= BM && a.scale > 0.f;
 }
 
-int pkv_launch_win_tc(const PkvWinArgs& a, int64_t Tq, pkv_dtype dt, int D, bool q4, void* stream) {
+int pkv_launch_win_tc(const PkvWinArgs& a, int64_t Tq, pkv_dtype dt, int D, bool q4, int* launches, void* stream) {
   cudaStream_t s = (cudaStream_t)stream;
-  if (q4) return D == 64 ? launch_t<64, true>(a, Tq, dt, s) : launch_t<128, true>(a, Tq, dt, s);
-  return D == 64 ? launch_t<64, false>(a, Tq, dt, s) : launch_t<128, false>(a, Tq, dt, s);
+  if (q4) return D == 64 ? launch_t<64, true>(a, Tq, dt, launches, s) : launch_t<128, true>(a, Tq, dt, launches, s);
+  return D == 64 ? launch_t<64, false>(a, Tq, dt, launches, s) : launch_t<128, false>(a, Tq, dt, launches, s);
 }

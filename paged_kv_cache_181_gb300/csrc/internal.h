@@ -128,7 +128,7 @@ int pkv_launch_gather_q4(const void* kp, const void* vp, int64_t num_blocks, con
 int pkv_launch_win_dec(const PkvWinArgs& a, pkv_dtype dt, int D, bool q4, void* stream);
 // tcgen05 path; for calls that pkv_win_tc_supports.
 bool pkv_win_tc_supports(const PkvWinArgs& a, pkv_dtype dt);
-int pkv_launch_win_tc(const PkvWinArgs& a, int64_t Tq, pkv_dtype dt, int D, bool q4, void* stream);
+int pkv_launch_win_tc(const PkvWinArgs& a, int64_t Tq, pkv_dtype dt, int D, bool q4, int* launches, void* stream);
 int pkv_launch_win_simt(const PkvWinArgs& a, pkv_dtype dt, int D, bool q4, void* stream);
 
 // Shared by those launchers (serving.cu).
@@ -144,5 +144,13 @@ int pkv_prepare_kernel(const void* kernel, int smem, int threads, int regs, PkvK
 int64_t pkv_visible_keys(const PkvWinArgs& a, int64_t tokens);
 // CTAs (1, 2, 4, 8 or 16) that share one item's `steps` key steps; a CTA's set-up and merge cost about `fixed` steps.
 int pkv_plan_cluster(const PkvKernelState& state, int64_t items, int64_t steps, double fixed);
+// The same for a kernel of one CTA per SM: `whole` items run as single CTAs, the others in a second launch of
+// clusters of `ctas` (0 whole items: one launch).
+struct PkvClusterPlan {
+  int64_t whole;
+  int ctas;
+};
+PkvClusterPlan pkv_plan_cluster_tail(const PkvKernelState& state, int64_t items, int64_t steps, double fixed);
+// `overlap`: the launch may start while the one before it on the stream still runs.
 int pkv_launch_cluster(const void* kernel, int64_t items, int ctas, int threads, size_t smem, void** args,
-                       void* stream);
+                       bool overlap, void* stream);

@@ -106,15 +106,15 @@ pkv_status win_impl(const char* fn, bool q4, const void* q, int64_t Tq, int Hq, 
   // Up to 32 query rows per kv head the memory-bound kernel, which reads each key once for all of them; beyond, tiles
   // of 256 rows on tcgen05.
   const int64_t rows = (int64_t)max_query_len * (Hq / Hkv);
-  int rc;
+  int rc, launches = 1;
   if (dt == PKV_F32 || (flags & PKV_FORCE_SIMT))
     rc = pkv_launch_win_simt(a, dt, D, q4, stream);
   else if (rows > 32 && num_blocks > 0 && pkv_win_tc_supports(a, dt))
-    rc = pkv_launch_win_tc(a, Tq, dt, D, q4, stream);
+    rc = pkv_launch_win_tc(a, Tq, dt, D, q4, &launches, stream);
   else
     rc = pkv_launch_win_dec(a, dt, D, q4, stream);
   if (rc) return pkv_fail(PKV_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString((cudaError_t)rc));
-  pkv_set_launches(1);
+  pkv_set_launches(launches);
   return PKV_OK;
 }
 
@@ -171,13 +171,17 @@ int64_t pkv_visible_keys(const PkvWinArgs& a, int64_t tokens) {
   return keys;
 }
 
-// The launch runs in waves of the clusters that fit the GPU at once; each CTA takes its share of the steps plus the
+namespace {
+
+struct Split {
+  int ctas;
+  double cost;
+};
+
+// A launch runs in waves of the clusters that fit the GPU at once; each CTA takes its share of the steps plus the
 // fixed cost.  The smallest estimate wins, a larger cluster only where it gains a tenth.
-int pkv_plan_cluster(const PkvKernelState& state, int64_t items, int64_t steps, double fixed) {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  int best = 1;
-  double best_cost = 1e300;
+Split best_split(const PkvKernelState& state, int dev, int64_t items, int64_t steps, double fixed) {
+  Split best{1, 1e300};
   for (int i = 0; i < 5; ++i) {
     const int c = 1 << i;
     const int64_t active = state.active[dev][i].load(std::memory_order_relaxed);
@@ -185,26 +189,55 @@ int pkv_plan_cluster(const PkvKernelState& state, int64_t items, int64_t steps, 
     if (c > 1 && (steps < 2 * c || items * c > kMaxGrid)) break;
     const int64_t at_once = active > 0 ? active : 152;
     const double cost = (double)((items + at_once - 1) / at_once) * ((double)((steps + c - 1) / c) + fixed);
-    if (cost < 0.9 * best_cost) best = c, best_cost = cost;
+    if (cost < 0.9 * best.cost) best = Split{c, cost};
   }
   return best;
 }
 
+int current_device() {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  return dev < 0 || dev >= 64 ? 0 : dev;
+}
+
+}  // namespace
+
+int pkv_plan_cluster(const PkvKernelState& state, int64_t items, int64_t steps, double fixed) {
+  return best_split(state, current_device(), items, steps, fixed).ctas;
+}
+
+// Whole waves of single CTAs, and a second launch that splits the items behind them, where that is estimated a
+// twentieth under one launch of equal clusters.
+PkvClusterPlan pkv_plan_cluster_tail(const PkvKernelState& state, int64_t items, int64_t steps, double fixed) {
+  const int dev = current_device();
+  const Split one = best_split(state, dev, items, steps, fixed);
+  const int64_t sms = state.active[dev][0].load(std::memory_order_relaxed);
+  if (sms > 0 && items > sms && items % sms) {
+    const int64_t waves = items / sms;
+    const Split tail = best_split(state, dev, items % sms, steps, fixed);
+    if (tail.ctas > 1 && waves * ((double)steps + fixed) + tail.cost < 0.95 * one.cost)
+      return PkvClusterPlan{waves * sms, tail.ctas};
+  }
+  return PkvClusterPlan{0, one.ctas};
+}
+
 int pkv_launch_cluster(const void* kernel, int64_t items, int ctas, int threads, size_t smem, void** args,
-                       void* stream) {
+                       bool overlap, void* stream) {
   if (items * ctas > kMaxGrid) return (int)cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * ctas));
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = (cudaStream_t)stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = overlap ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
   const cudaError_t last = cudaGetLastError();
   return (int)(e != cudaSuccess ? e : last);

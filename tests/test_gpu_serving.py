@@ -221,7 +221,7 @@ def attention(lib, rows, hq, hkv, d, dtype, window, sinks, q4=False, seed=0, fla
     fn(q.cuda(), kp.cuda(), vp.cuda(), torch.from_numpy(table).cuda(), torch.from_numpy(qsl).cuda(),
        torch.tensor(lens, dtype=torch.int32).cuda(), max(1, max(r[0] for r in rows)), max(lens), scale, window=window,
        sinks=sinks, out=out, flags=flags | lib.PKV_CHECK_BOUNDS)
-    assert lib.check() == 0 and lib.last_launches() == 1
+    assert lib.check() == 0 and lib.last_launches() in (1, 2)
     out = out.double().cpu().numpy()
     assert (out[qsl[-1]:] == 77).all()
     half = {"f32": 0.0, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dtype]
