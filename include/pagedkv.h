@@ -314,10 +314,14 @@ PKV_API pkv_status paged_kv_gather_q4(const void* key_pool, const void* value_po
  * Table entries of blocks that no query of the row sees are not read: evicted blocks may hold any id.  Keys and
  * values that no query of the row sees do not enter any output, whatever they hold; a NaN or an infinity in a
  * value that some query of the row sees may also reach the row's other queries.
- * No workspace: CTAs that share a query tile's keys form a cluster and merge through its shared memory.  One launch,
- * or two where a prompt's query tiles leave a last wave partly filled (the second splits that wave's tiles).
+ * CTAs that share a query tile's keys form a cluster and merge through its shared memory: one launch, or two where a
+ * prompt's query tiles leave a last wave partly filled (the second splits that wave's tiles).  Where sequences and
+ * heads are too few for clusters to fill the GPU, more CTAs share a tile and a second launch combines their partial
+ * results from the workspace (paged_attn_window_workspace_size); without one, clusters do.
  * Out rows past query_start_loc[B] are left as they are.
  *   window, sinks  >= 0
+ *   workspace      device, 16-byte aligned, or NULL; used by this call alone until it has run; nothing in it has to
+ *                  start at zero.  One smaller than the size below is not used.
  *   softmax_scale  finite; > 0 for bf16/f16 unless flags holds PKV_FORCE_SIMT
  *   flags          PKV_CHECK_BOUNDS (bad block ids, query lengths, key lengths past the table or max_seq_len),
  *                  PKV_FORCE_SIMT (the fp32 CUDA-core kernel); others are ignored
@@ -327,7 +331,15 @@ PKV_API pkv_status paged_attn_window(const void* q, int64_t Tq, int Hq, const vo
                                      int64_t num_blocks, int block_size, int Hkv, int D, pkv_dtype dt,
                                      const int32_t* block_table, int B, int W, const int32_t* query_start_loc,
                                      const int32_t* seq_lens, int max_query_len, int max_seq_len, float softmax_scale,
-                                     int window, int sinks, void* out, uint32_t flags, void* stream);
+                                     int window, int sinks, void* out, void* workspace, size_t ws_bytes, uint32_t flags,
+                                     void* stream);
+
+/*
+ * paged_attn_window_workspace_size -- bytes of workspace that paged_attn_window (q4 == 0) or paged_attn_q4 (q4 != 0)
+ * would use for a call of these sizes on the current device; 0 when it would use none (and for sizes it refuses).
+ */
+PKV_API size_t paged_attn_window_workspace_size(int64_t num_blocks, int Hq, int Hkv, int D, pkv_dtype dt, int q4, int B,
+                                                int max_query_len, int max_seq_len, int window, int sinks);
 
 /*
  * paged_attn_q4 -- paged_attn_window over 4-bit pools; dt is q's and out's type.
@@ -336,7 +348,8 @@ PKV_API pkv_status paged_attn_q4(const void* q, int64_t Tq, int Hq, const void* 
                                  int64_t num_blocks, int block_size, int Hkv, int D, pkv_dtype dt,
                                  const int32_t* block_table, int B, int W, const int32_t* query_start_loc,
                                  const int32_t* seq_lens, int max_query_len, int max_seq_len, float softmax_scale,
-                                 int window, int sinks, void* out, uint32_t flags, void* stream);
+                                 int window, int sinks, void* out, void* workspace, size_t ws_bytes, uint32_t flags,
+                                 void* stream);
 
 /*
  * paged_attn_workspace_size -- bytes of workspace paged_attn_varlen may use

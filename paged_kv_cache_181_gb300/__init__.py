@@ -15,7 +15,7 @@ _API = (
     "PKV_SEG_FULL", "PKV_SPLITS", "PkvError", "block_table_row", "build_segments", "check", "last_error",
     "PKV_ROPE_INTERLEAVED", "paged_attn_q4", "paged_attn_varlen", "paged_attn_window", "paged_kv_append",
     "paged_kv_append_q4", "paged_kv_gather_q4", "paged_kv_write", "q4_block_bytes", "slot_mapping", "sm_count", "table_width", "visible_window",
-    "workspace_size",
+    "window_workspace_size", "workspace_size",
 )
 
 __all__ = list(_API)
@@ -25,5 +25,6 @@ def __getattr__(name):
     if name in _API:
         from . import _lib
 
-        return getattr(_lib, name)
+        value = globals()[name] = getattr(_lib, name)  # found directly from now on
+        return value
     raise AttributeError(name)

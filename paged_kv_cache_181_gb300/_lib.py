@@ -35,7 +35,7 @@ EXPORTS = (
     "paged_attn_varlen", "pkv_check", "pkv_sm_count", "pkv_last_launches", "paged_attn_varlen_noalloc",
     "paged_kv_gather", "paged_kv_write_attn", "pkv_selftest_wait", "pkv_last_split_plan",
     "paged_kv_append", "pkv_q4_block_bytes", "paged_kv_append_q4", "paged_kv_gather_q4", "paged_attn_window",
-    "paged_attn_q4",
+    "paged_attn_q4", "paged_attn_window_workspace_size",
 )
 
 
@@ -91,6 +91,7 @@ def _load() -> C.CDLL:
         "paged_attn_varlen_noalloc": (C.c_int, [vp, C.c_int64, C.c_int, vp, vp, C.c_int64, C.c_int, C.c_int, C.c_int,
                                                 C.c_int, vp, C.c_int, C.c_int, vp, vp, C.c_int, C.c_int, C.c_float, vp,
                                                 vp, vp, C.c_uint32, vp]),
+        "paged_attn_window_workspace_size": (C.c_size_t, [C.c_int64] + [C.c_int] * 10),
         "pkv_q4_block_bytes": (C.c_size_t, [C.c_int]),
         "paged_kv_gather_q4": (C.c_int, [vp, vp, C.c_int64, vp, C.c_int, C.c_int, C.c_int, C.c_int, vp, vp, C.c_int64,
                                          C.c_int, C.c_int, C.c_int, C.c_uint32, vp]),
@@ -100,8 +101,8 @@ def _load() -> C.CDLL:
                                C.c_int, vp, vp, vp, C.c_int64, C.c_int, C.c_int, C.c_int, C.c_uint32, vp])
     for name in ("paged_attn_window", "paged_attn_q4"):
         sig[name] = (C.c_int, [vp, C.c_int64, C.c_int, vp, vp, C.c_int64, C.c_int, C.c_int, C.c_int, C.c_int, vp,
-                               C.c_int, C.c_int, vp, vp, C.c_int, C.c_int, C.c_float, C.c_int, C.c_int, vp, C.c_uint32,
-                               vp])
+                               C.c_int, C.c_int, vp, vp, C.c_int, C.c_int, C.c_float, C.c_int, C.c_int, vp, vp,
+                               C.c_size_t, C.c_uint32, vp])
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -559,7 +560,7 @@ def paged_kv_gather_q4(key_pool, value_pool, block_table, stage_k, stage_v, *, f
 
 
 def _attn_window(fn: str, entry, q4: bool, q, key_pool, value_pool, block_table, query_start_loc, seq_lens,
-                 max_query_len, max_seq_len, softmax_scale, window, sinks, out, flags, block_size, stream):
+                 max_query_len, max_seq_len, softmax_scale, window, sinks, out, workspace, flags, block_size, stream):
     torch = _torch()
     shape, dtype, pool_shape, table_shape = q.shape, q.dtype, key_pool.shape, block_table.shape
     code = _code(fn, dtype)
@@ -591,34 +592,56 @@ def _attn_window(fn: str, entry, q4: bool, q, key_pool, value_pool, block_table,
     if block_table.dtype != i32 or query_start_loc.dtype != i32 or seq_lens.dtype != i32:
         raise ValueError(f"{fn}: metadata must be int32")
     dev = _check_device(fn, (q, key_pool, value_pool, block_table, query_start_loc, seq_lens, out))
+    ws_at = ws_bytes = 0
+    if workspace is not None:
+        _check_device(fn, (q, workspace))
+        ws_at, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif B * hkv < 256 and code:  # more items than that never take one
+        ws_bytes = lib.paged_attn_window_workspace_size(blocks, hq, hkv, d, code, q4, B, max_query_len, max_seq_len,
+                                                        window, sinks)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            ws_at = workspace.data_ptr()
+            if stream is not None:
+                workspace.record_stream(stream)
     status = entry(q.data_ptr(), Tq, hq, key_pool.data_ptr(), value_pool.data_ptr(), blocks, block_size, hkv, d, code,
                    block_table.data_ptr(), B, W, query_start_loc.data_ptr(), seq_lens.data_ptr(), int(max_query_len),
-                   int(max_seq_len), float(softmax_scale), int(window), int(sinks), out.data_ptr(), flags,
+                   int(max_seq_len), float(softmax_scale), int(window), int(sinks), out.data_ptr(), ws_at, ws_bytes, flags,
                    _raw_stream(dev) if stream is None else stream.cuda_stream)
     if status:
         _ok(status)
     return out
 
 
+def window_workspace_size(num_blocks: int, num_heads: int, num_kv_heads: int, head_dim: int, dtype, batch: int,
+                          max_query_len: int, max_seq_len: int, window: int = 0, sinks: int = 0, q4: bool = False) -> int:
+    """Bytes of workspace that paged_attn_window (``q4``: paged_attn_q4) would use for these sizes; 0: none."""
+    return int(lib.paged_attn_window_workspace_size(int(num_blocks), int(num_heads), int(num_kv_heads), int(head_dim),
+                                                    _code("window_workspace_size", dtype), int(q4), int(batch),
+                                                    int(max_query_len), int(max_seq_len), int(window), int(sinks)))
+
+
 def paged_attn_window(q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len: int,
                       max_seq_len: int, softmax_scale: float, *, window: int = 0, sinks: int = 0, out=None,
-                      flags: int = 0, block_size: int = 16, stream=None):
+                      workspace=None, flags: int = 0, block_size: int = 16, stream=None):
     """Causal paged attention: query p sees key j <= p when ``window == 0``, ``j < sinks`` or ``p - j < window``.
 
     Pools are ``[num_blocks * 16, Hkv, D]`` of q's dtype; a row's queries are the last of its keys.  Returns ``out``.
+    ``workspace`` is scratch of ``window_workspace_size`` bytes that no other call uses at the same time; without one
+    the call takes what it needs from torch's allocator.
     """
     return _attn_window("paged_attn_window", lib.paged_attn_window, False, q, key_pool, value_pool, block_table,
                         query_start_loc, seq_lens, max_query_len, max_seq_len, softmax_scale, window, sinks, out,
-                        flags, block_size, stream)
+                        workspace, flags, block_size, stream)
 
 
 def paged_attn_q4(q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len: int,
                   max_seq_len: int, softmax_scale: float, *, window: int = 0, sinks: int = 0, out=None,
-                  flags: int = 0, block_size: int = 16, stream=None):
+                  workspace=None, flags: int = 0, block_size: int = 16, stream=None):
     """paged_attn_window over 4-bit pools (uint8 ``[num_blocks, Hkv, q4_block_bytes(D)]``); returns ``out``."""
     return _attn_window("paged_attn_q4", lib.paged_attn_q4, True, q, key_pool, value_pool, block_table,
                         query_start_loc, seq_lens, max_query_len, max_seq_len, softmax_scale, window, sinks, out,
-                        flags, block_size, stream)
+                        workspace, flags, block_size, stream)
 
 
 def check(stream=None) -> int:

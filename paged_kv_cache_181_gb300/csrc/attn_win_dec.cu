@@ -10,7 +10,8 @@
 // values: the sum over channels may run in any order, so a lane loads 16 contiguous bytes of a key and uses them as
 // two k-steps' operands, with Q permuted to match; a V operand pairs two keys per register, which one byte
 // permute per pair makes from two keys' loads.  P^T comes from S^T's registers by one 8x8 transpose per 8 keys.
-// Loads of the next page are issued as soon as the registers of this page's K (then V) are used up.
+// Loads of the next step (one page; two of a 4-bit pool) are issued as soon as the registers of this step's K (then V)
+// are used up.
 //
 // A row's maximum is raised only when a score exceeds it by 2^8 (one vote per page, no shuffles otherwise);
 // probabilities stay below 2^8, exact in their 16-bit type's range.  P is rounded to the value type for the product,
@@ -93,20 +94,32 @@ struct Page16 {
   static PKV_DEVINLINE int64_t page_bytes(int Hkv) { return (int64_t)16 * Hkv * D * 2; }
   static PKV_DEVINLINE int64_t head_bytes(int kvh) { return (int64_t)kvh * D * 2; }
 
-  PKV_DEVINLINE void load_k(const uint8_t* head, int Hkv, int g, int t, const bool (&live)[2]) {
+  // Keys whose bit is clear in `seen` (bit k: key k of the page) are not loaded and count as zeros.
+  PKV_DEVINLINE void load_k(const uint8_t* head, int Hkv, int g, int t, unsigned seen) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const uint8_t* p = head + (int64_t)(g + 8 * r) * Hkv * D * 2 + t * 16;
+      if (seen == 0xffffu || ((seen >> (g + 8 * r)) & 1)) {
 #pragma unroll
-      for (int i = 0; i < NK; ++i) k[r][i] = live[r] ? ld16(p + 64 * i) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < NK; ++i) k[r][i] = ld16(p + 64 * i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NK; ++i) k[r][i] = make_uint4(0, 0, 0, 0);
+      }
     }
   }
-  PKV_DEVINLINE void load_v(const uint8_t* head, int Hkv, int g, int t, const bool (&live)[4]) {
+  PKV_DEVINLINE void load_v(const uint8_t* head, int Hkv, int g, int t, unsigned seen) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const uint8_t* p = head + (int64_t)(2 * t + (r & 1) + (r >> 1) * 8) * Hkv * D * 2 + g * 16;
+      const int key = 2 * t + (r & 1) + (r >> 1) * 8;
+      const uint8_t* p = head + (int64_t)key * Hkv * D * 2 + g * 16;
+      if (seen == 0xffffu || ((seen >> key) & 1)) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[r][i] = live[r] ? ld16(p + 128 * i) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < NV; ++i) v[r][i] = ld16(p + 128 * i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[r][i] = make_uint4(0, 0, 0, 0);
+      }
     }
   }
   static PKV_DEVINLINE uint32_t word(const uint4& x, int i) { return i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w; }
@@ -151,14 +164,11 @@ struct PageQ4 {
   static PKV_DEVINLINE int64_t page_bytes(int Hkv) { return (int64_t)Hkv * F::kRecord; }
   static PKV_DEVINLINE int64_t head_bytes(int kvh) { return (int64_t)kvh * F::kRecord; }
 
-  PKV_DEVINLINE void load_k(const uint8_t* rec, int, int g, int t, const bool (&live)[2]) {
+  PKV_DEVINLINE void load_k(const uint8_t* rec, int, int g, int t, unsigned seen) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int key = g + 8 * r;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) k[r][i] = 0;
-      kp[r] = 0;
-      if (live[r]) {
+      if (seen == 0xffffu || ((seen >> key) & 1)) {
         if (D == 128) {
           const uint4 x = ld16(rec + key * F::kRowBytes + t * 16);
           k[r][0] = x.x, k[r][1] = x.y, k[r][D / 32 - 2] = x.z, k[r][D / 32 - 1] = x.w;
@@ -167,17 +177,18 @@ struct PageQ4 {
           k[r][0] = x.x, k[r][1] = x.y;
         }
         kp[r] = ld4(rec + F::kPairs + (key * F::kGroups + (D == 128 ? t : t >> 1)) * 4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) k[r][i] = 0;
+        kp[r] = 0;
       }
     }
   }
-  PKV_DEVINLINE void load_v(const uint8_t* rec, int, int g, int t, const bool (&live)[4]) {
+  PKV_DEVINLINE void load_v(const uint8_t* rec, int, int g, int t, unsigned seen) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int key = 2 * t + (r & 1) + (r >> 1) * 8;
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) v[r][i] = 0;
-      vp[r] = 0;
-      if (live[r]) {
+      if (seen == 0xffffu || ((seen >> key) & 1)) {
         if (D == 128) {
           const uint2 x = ld8(rec + key * F::kRowBytes + g * 8);
           v[r][0] = x.x, v[r][D / 64 - 1] = x.y;
@@ -185,6 +196,10 @@ struct PageQ4 {
           v[r][0] = ld4(rec + key * F::kRowBytes + g * 4);
         }
         vp[r] = ld4(rec + F::kPairs + (key * F::kGroups + (D == 128 ? g >> 1 : g >> 2)) * 4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) v[r][i] = 0;
+        vp[r] = 0;
       }
     }
   }
@@ -244,8 +259,14 @@ struct DecSmem {
   uint4 q[NT > 2 ? NT : 1][NT > 2 ? D / 32 : 1][32];  // Q's B operands, when they do not fit in registers
 };
 
-template <typename T, bool POOLQ4, int D, int NT, int PF>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_win_dec_kernel(const PkvWinArgs a) {
+// Partial results of one split of an item, for the combine: [item][split] x (ROWS x D sums, ROWS maxima, ROWS sums).
+template <int D, int NT>
+constexpr int64_t kPartialFloats = 8 * NT * (D + 2);
+
+// PG pages per step.  `splits` > 1: that many CTAs (no clusters) share an item and leave partials in `ws`.
+template <typename T, bool POOLQ4, int D, int NT, int PG>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+    attn_win_dec_kernel(const PkvWinArgs a, const int splits, float* __restrict__ ws) {
   constexpr bool BF16 = !POOLQ4 && sizeof(T) == 2 && !std::is_same<T, __half>::value;
   constexpr int ROWS = 8 * NT;
   constexpr bool QS = NT > 2;
@@ -255,8 +276,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_win_dec_kernel
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gl = lane >> 2, tl = lane & 3;
   const int g = a.Hq / a.Hkv;
   const int n_qt = (int)(((int64_t)a.max_query_len * g + ROWS - 1) / ROWS);
-  const uint32_t rank = cluster_rank(), n_cta = cluster_size();
-  uint32_t item = blockIdx.x / n_cta;
+  if (splits > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t share = splits > 1 ? (uint32_t)splits : cluster_size();  // CTAs of one item
+  const uint32_t rank = splits > 1 ? blockIdx.x % share : cluster_rank();
+  uint32_t item = blockIdx.x / share;
+  const uint32_t item_id = item;
   const int kvh = item % a.Hkv;
   item /= a.Hkv;
   const int qt = item % n_qt, b = item / n_qt;
@@ -331,109 +355,132 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_win_dec_kernel
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
 
-  // This warp's pages: gw, gw + step, ...; their block ids are fetched 32 at a time, one per lane.
-  const int gw = rank * kWarps + warp, step = n_cta * kWarps;
-  const int n = pg.n > gw ? (pg.n - gw + step - 1) / step : 0;
+  // This warp's pages: gw, gw + stride, ...; their block ids are fetched 32 at a time, one per lane.
+  const int gw = rank * kWarps + warp, stride = share * kWarps;
+  const int n = pg.n > gw ? (pg.n - gw + stride - 1) / stride : 0;
   const int64_t page_bytes = Page::page_bytes(a.Hkv), head_bytes = Page::head_bytes(kvh);
   int ids = 0;
-  auto block_of = [&](int i) -> int {  // i counts up by one from call to call
-    if ((i & 31) == 0) {
-      const int v = gw + (i + lane) * step;
-      ids = i + lane < n ? win_block(a, b, pg.page(v)) : 0;
+  Page page[PG];
+  const uint8_t* vhead[PG];
+  int first[PG];       // first key of the page
+  unsigned seen[PG];   // its keys that some row sees
+  auto issue_k = [&](int i0) {  // pages i0 .. i0 + PG - 1 of the warp; i0 counts up by PG from call to call
+    if ((i0 & 31) == 0) {
+      const int v = gw + (i0 + lane) * stride;
+      ids = i0 + lane < n ? win_block(a, b, pg.page(v)) : 0;
     }
-    return __shfl_sync(0xffffffffu, ids, i & 31);
-  };
-  Page pages[PF];
-  const uint8_t* vhead[PF];
-  int first[PF];  // first key of the page
-  auto issue_k = [&](int i, int s) {
-    if (i >= n) return;
-    const int64_t at = (int64_t)block_of(i) * page_bytes + head_bytes;
-    vhead[s] = (const uint8_t*)a.v_pool + at;
-    first[s] = pg.page(gw + i * step) * 16;
-    const bool live[2] = {pg.any(first[s] + gl), pg.any(first[s] + gl + 8)};
-    pages[s].load_k((const uint8_t*)a.k_pool + at, a.Hkv, gl, tl, live);
-  };
-  auto issue_v = [&](int i, int s) {
-    if (i >= n) return;
-    bool live[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) live[r] = pg.any(first[s] + 2 * tl + (r & 1) + (r >> 1) * 8);
-    pages[s].load_v(vhead[s], a.Hkv, gl, tl, live);
+    for (int u = 0; u < PG; ++u) {
+      const int i = i0 + u;
+      const int64_t at = (int64_t)__shfl_sync(0xffffffffu, ids, i & 31) * page_bytes + head_bytes;
+      const int j0 = pg.page(gw + i * stride) * 16;
+      unsigned bits = 0xffffu;
+      if (i >= n)
+        bits = 0;
+      else if (!(j0 + 15 < pg.hi && (j0 >= pg.lo || j0 + 15 < pg.sinks))) {
+        bits = __ballot_sync(0xffffffffu, pg.any(j0 + (lane & 15))) & 0xffffu;
+      }
+      seen[u] = bits;
+      first[u] = i < n ? j0 : 0x3ffffff0;
+      vhead[u] = (const uint8_t*)a.v_pool + at;
+      page[u].load_k((const uint8_t*)a.k_pool + at, a.Hkv, gl, tl, bits);
+    }
   };
+  auto issue_v = [&]() {
 #pragma unroll
-  for (int s = 0; s < PF; ++s) {
-    issue_k(s, s);
-    issue_v(s, s);
+    for (int u = 0; u < PG; ++u) page[u].load_v(vhead[u], a.Hkv, gl, tl, seen[u]);
+  };
+  if (n > 0) {
+    issue_k(0);
+    issue_v();
   }
-
-  for (int i0 = 0; i0 < n; i0 += PF) {
+  for (int i = 0; i < n; i += PG) {
+    float x[PG][NT][4] = {};
 #pragma unroll
-    for (int s = 0; s < PF; ++s) {
-      const int i = i0 + s;
-      if (i >= n) break;
-      float x[NT][4] = {};
-      pages[s].k_steps([&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+    for (int u = 0; u < PG; ++u)
+      page[u].k_steps([&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint4 qq = QS ? sm.q[nt][k >> 1][lane] : q[QS ? 0 : nt][k >> 1];
-          mma<BF16>(x[nt], a0, a1, a2, a3, (k & 1) ? qq.z : qq.x, (k & 1) ? qq.w : qq.y);
+          mma<BF16>(x[u][nt], a0, a1, a2, a3, (k & 1) ? qq.z : qq.x, (k & 1) ? qq.w : qq.y);
         }
       });
-      const int j0 = first[s];
-      issue_k(i + PF, s);  // K's registers are free; first[s] and vhead[s] now belong to the next page
-      const bool all = j0 + 15 <= p_first && (a.window == 0 || j0 + 15 < a.sinks || p_last - j0 < a.window);
+    bool all = true;  // every row sees every key
+    int j0[PG];
+#pragma unroll
+    for (int u = 0; u < PG; ++u) {
+      j0[u] = first[u];
+      all = all && j0[u] + 15 <= p_first && (a.window == 0 || j0[u] + 15 < a.sinks || p_last - j0[u] < a.window);
+    }
+    const bool more = i + PG < n;
+    if (more) issue_k(i + PG);  // K's registers are free; V's still hold this step's
+#pragma unroll
+    for (int u = 0; u < PG; ++u)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[nt][c] *= f[nt][c & 1];
-      if (!all) {
+        for (int c = 0; c < 4; ++c) x[u][nt][c] *= f[nt][c & 1];
+    if (!all) {
+#pragma unroll
+      for (int u = 0; u < PG; ++u)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            x[nt][c] = win_sees(p[nt][c & 1], j0 + gl + 8 * (c >> 1), a.window, a.sinks) ? x[nt][c] : -INFINITY;
+            x[u][nt][c] =
+                win_sees(p[nt][c & 1], j0[u] + gl + 8 * (c >> 1), a.window, a.sinks) ? x[u][nt][c] : -INFINITY;
+    }
+    float top[NT][2];
+    bool grow = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        top[nt][c] = fmaxf(x[0][nt][c], x[0][nt][c + 2]);
+#pragma unroll
+        for (int u = 1; u < PG; ++u) top[nt][c] = ptx::max3(top[nt][c], x[u][nt][c], x[u][nt][c + 2]);
+        grow = grow || top[nt][c] > m[nt][c] + kRescale;
       }
-      bool grow = false;
+    if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) grow = grow || fmaxf(x[nt][c], x[nt][c + 2]) > m[nt][c] + kRescale;
-      if (__any_sync(0xffffffffu, grow)) {
+        for (int c = 0; c < 2; ++c) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int k = 4; k < 32; k <<= 1) top[nt][c] = fmaxf(top[nt][c], __shfl_xor_sync(0xffffffffu, top[nt][c], k));
+          if (top[nt][c] > m[nt][c]) {
+            const float alpha = ptx::ex2(m[nt][c] - top[nt][c]);  // 0 from -inf
+            m[nt][c] = top[nt][c];
+            l[nt][c] *= alpha;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(x[nt][c], x[nt][c + 2]);
-#pragma unroll
-            for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-            if (top > m[nt][c]) {
-              const float alpha = ptx::ex2(m[nt][c] - top);  // 0 from -inf
-              m[nt][c] = top;
-              l[nt][c] *= alpha;
-#pragma unroll
-              for (int e = 0; e < D / 16; ++e) o[nt][e][c] *= alpha, o[nt][e][c + 2] *= alpha;
-            }
+            for (int e = 0; e < D / 16; ++e) o[nt][e][c] *= alpha, o[nt][e][c + 2] *= alpha;
           }
-      }
-      uint32_t b0[NT], b1[NT];
+        }
+    }
+    uint32_t b0[PG][NT], b1[PG][NT];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt) {
+      float mu[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) mu[c] = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
+#pragma unroll
+      for (int u = 0; u < PG; ++u) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float mu = m[nt][c & 1] == -INFINITY ? 0.f : m[nt][c & 1];
-          x[nt][c] = ptx::ex2(x[nt][c] - mu);
-          l[nt][c & 1] += x[nt][c];
+          x[u][nt][c] = ptx::ex2(x[u][nt][c] - mu[c & 1]);
+          l[nt][c & 1] += x[u][nt][c];
         }
-        b0[nt] = transpose8(pack<BF16>(x[nt][0], x[nt][1]));
-        b1[nt] = transpose8(pack<BF16>(x[nt][2], x[nt][3]));
+        b0[u][nt] = transpose8(pack<BF16>(x[u][nt][0], x[u][nt][1]));
+        b1[u][nt] = transpose8(pack<BF16>(x[u][nt][2], x[u][nt][3]));
       }
-      pages[s].v_tiles([&](int e, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma<BF16>(o[nt][e], a0, a1, a2, a3, b0[nt], b1[nt]);
-      });
-      issue_v(i + PF, s);
     }
+#pragma unroll
+    for (int u = 0; u < PG; ++u)
+      page[u].v_tiles([&](int e, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma<BF16>(o[nt][e], a0, a1, a2, a3, b0[u][nt], b1[u][nt]);
+      });
+    if (more) issue_v();
   }
 
   // ---------------------------------------------------------------- merge: warps, then the cluster's CTAs
@@ -466,47 +513,135 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_win_dec_kernel
       acc += k * sm.o[w][r][c];
       sum += k * sm.wl[w][r];
     }
+    if (splits > 1) {
+      float* part = ws + ((int64_t)item_id * splits + rank) * kPartialFloats<D, NT>;
+      part[r * D + c] = acc;
+      if (c == 0) part[ROWS * D + r] = top, part[ROWS * (D + 1) + r] = sum;
+      continue;
+    }
     sm.o[0][r][c] = acc;  // read and written by this thread alone
     if (c == 0) sm.m[r] = top, sm.l[r] = sum;
   }
+  if (splits > 1) return;
   win_merge_store<T, D>(&sm.o[0][0][0], DecSmem<D, NT>::kStride, sm.m, sm.l, rows, r0, g, kvh, a.Hq, row.q0, (T*)a.out,
                         tid, kThreads);
 }
 
+// Rows of the items that several CTAs share: one block per (item, row), its two halves each taking every other split.
+// A programmatic dependent launch: its blocks may be in place before the attention's last CTAs are done.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(D) attn_win_combine_kernel(const PkvWinArgs a, const int splits,
+                                                             const float* __restrict__ ws) {
+  constexpr int ROWS = 8 * NT, PAIRS = D / 2;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int g = a.Hq / a.Hkv;
+  const int n_qt = (int)(((int64_t)a.max_query_len * g + ROWS - 1) / ROWS);
+  const int r = blockIdx.x % ROWS;
+  uint32_t item = blockIdx.x / ROWS;
+  const float* part = ws + (int64_t)item * splits * kPartialFloats<D, NT>;
+  const int kvh = item % a.Hkv;
+  item /= a.Hkv;
+  const int qt = item % n_qt, b = item / n_qt;
+  const WinRow row = win_row(a, b, false);
+  const int64_t at = (int64_t)qt * ROWS + r;
+  if (at >= (int64_t)row.Sq * g) return;
+  __shared__ float sm_w[64];
+  __shared__ float2 sm_x[PAIRS];
+  __shared__ float sm_sum;
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (tid < 32) {  // the splits' weights
+    float mk[2], lk[2], top = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = lane + 32 * h;
+      mk[h] = k < splits ? part[k * kPartialFloats<D, NT> + ROWS * D + r] : -INFINITY;
+      lk[h] = k < splits ? part[k * kPartialFloats<D, NT> + ROWS * (D + 1) + r] : 0.f;
+      top = fmaxf(top, mk[h]);
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    float sum = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float w = mk[h] == top ? 1.f : ptx::ex2(mk[h] - top);
+      sm_w[lane + 32 * h] = w;
+      sum += w * lk[h];
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    if (lane == 0) sm_sum = sum;
+  }
+  __syncthreads();
+  const int half = tid / PAIRS, c = tid % PAIRS;
+  float2 x = make_float2(0.f, 0.f);
+#pragma unroll 8
+  for (int k = half; k < splits; k += 2) {
+    const float2 v = *reinterpret_cast<const float2*>(part + k * kPartialFloats<D, NT> + r * D + 2 * c);
+    x.x += sm_w[k] * v.x, x.y += sm_w[k] * v.y;
+  }
+  if (half) sm_x[c] = x;
+  __syncthreads();
+  if (half == 0) {
+    const float sum = sm_sum, inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t tok = (int64_t)row.q0 + at / g;
+    store_pair<T>((T*)a.out + (tok * a.Hq + kvh * g + at % g) * D + 2 * c, (x.x + sm_x[c].x) * inv,
+                  (x.y + sm_x[c].y) * inv);
+  }
+}
+
 template <typename T, bool POOLQ4, int D, int NT>
-int launch(const PkvWinArgs& a, cudaStream_t s) {
-  constexpr int PF = POOLQ4 ? 2 : 1;
-  auto kernel = attn_win_dec_kernel<T, POOLQ4, D, NT, PF>;
+int launch(const PkvWinArgs& a, void* workspace, size_t ws_bytes, size_t* ws_wanted, int* launches, cudaStream_t s) {
+  constexpr int PG = POOLQ4 && NT <= 2 ? 2 : 1;
+  auto kernel = attn_win_dec_kernel<T, POOLQ4, D, NT, PG>;
   const size_t smem = sizeof(DecSmem<D, NT>);
   static PkvKernelState state;
-  const int rc = pkv_prepare_kernel((const void*)kernel, (int)smem, kThreads, 0, state);
+  int rc = pkv_prepare_kernel((const void*)kernel, (int)smem, kThreads, 0, state);
   if (rc) return rc;
   const int g = a.Hq / a.Hkv;
   const int64_t items = (int64_t)a.B * a.Hkv * (((int64_t)a.max_query_len * g + 8 * NT - 1) / (8 * NT));
-  const int ctas = pkv_plan_cluster(state, items, pkv_visible_keys(a, 8 * NT / g + 1) / (16 * kWarps) + 1, 4.0);
-  void* args[] = {const_cast<PkvWinArgs*>(&a)};
-  return pkv_launch_cluster((const void*)kernel, items, ctas, kThreads, smem, args, false, s);
+  const int64_t steps = pkv_visible_keys(a, 8 * NT / g + 1) / (16 * kWarps) + 1;
+  // Items too few for clusters of 16 to fill the GPU: more CTAs per item, and the combine launch.
+  int splits = pkv_plan_splits(state, items, steps, 4.0, 3.0);
+  const size_t need = splits > 1 ? (size_t)(items * splits * kPartialFloats<D, NT> * 4) : 0;
+  if (ws_wanted) {
+    *ws_wanted = need;
+    return 0;
+  }
+  if (need > ws_bytes || !workspace) splits = 1;
+  float* ws = splits > 1 ? (float*)workspace : nullptr;
+  void* args[] = {const_cast<PkvWinArgs*>(&a), &splits, &ws};
+  const int ctas = splits > 1 ? 1 : pkv_plan_cluster(state, items, steps, 4.0);
+  *launches = 1;
+  rc = pkv_launch_cluster((const void*)kernel, splits > 1 ? items * splits : items, ctas, kThreads, smem, args, false, s);
+  if (rc || splits == 1) return rc;
+  *launches = 2;
+  return pkv_launch_cluster((const void*)attn_win_combine_kernel<T, D, NT>, items * 8 * NT, 1, D, 0, args, true, s);
 }
 
 template <typename T, bool POOLQ4, int D>
-int launch_rows(const PkvWinArgs& a, cudaStream_t s) {
+int launch_rows(const PkvWinArgs& a, void* ws, size_t bytes, size_t* wanted, int* launches, cudaStream_t s) {
   const int64_t rows = (int64_t)a.max_query_len * (a.Hq / a.Hkv);
-  if (rows <= 8) return launch<T, POOLQ4, D, 1>(a, s);
-  if (rows <= 16) return launch<T, POOLQ4, D, 2>(a, s);
-  return launch<T, POOLQ4, D, 4>(a, s);
+  if (rows <= 8) return launch<T, POOLQ4, D, 1>(a, ws, bytes, wanted, launches, s);
+  if (rows <= 16) return launch<T, POOLQ4, D, 2>(a, ws, bytes, wanted, launches, s);
+  return launch<T, POOLQ4, D, 4>(a, ws, bytes, wanted, launches, s);
 }
 
 template <typename T>
-int launch_pool(const PkvWinArgs& a, int D, bool q4, cudaStream_t s) {
-  if (q4) return D == 64 ? launch_rows<T, true, 64>(a, s) : launch_rows<T, true, 128>(a, s);
-  return D == 64 ? launch_rows<T, false, 64>(a, s) : launch_rows<T, false, 128>(a, s);
+int launch_pool(const PkvWinArgs& a, int D, bool q4, void* ws, size_t bytes, size_t* wanted, int* launches,
+                cudaStream_t s) {
+  if (q4)
+    return D == 64 ? launch_rows<T, true, 64>(a, ws, bytes, wanted, launches, s)
+                   : launch_rows<T, true, 128>(a, ws, bytes, wanted, launches, s);
+  return D == 64 ? launch_rows<T, false, 64>(a, ws, bytes, wanted, launches, s)
+                 : launch_rows<T, false, 128>(a, ws, bytes, wanted, launches, s);
 }
 
 }  // namespace
 
-int pkv_launch_win_dec(const PkvWinArgs& a, pkv_dtype dt, int D, bool q4, void* stream) {
+int pkv_launch_win_dec(const PkvWinArgs& a, pkv_dtype dt, int D, bool q4, void* workspace, size_t ws_bytes,
+                       size_t* ws_wanted, int* launches, void* stream) {
   cudaStream_t s = (cudaStream_t)stream;
-  if (dt == PKV_BF16) return launch_pool<__nv_bfloat16>(a, D, q4, s);
-  if (dt == PKV_F16) return launch_pool<__half>(a, D, q4, s);
+  if (dt == PKV_BF16) return launch_pool<__nv_bfloat16>(a, D, q4, workspace, ws_bytes, ws_wanted, launches, s);
+  if (dt == PKV_F16) return launch_pool<__half>(a, D, q4, workspace, ws_bytes, ws_wanted, launches, s);
   return (int)cudaErrorInvalidValue;
 }

@@ -782,9 +782,7 @@ int launch_t(const PkvWinArgs& a, int64_t Tq, pkv_dtype dt, int* launches, cudaS
 
 }  // namespace
 
-bool pkv_win_tc_supports(const PkvWinArgs& a, pkv_dtype dt) {
-  return (dt == PKV_BF16 || dt == PKV_F16) && a.Hq / a.Hkv <= BM && a.scale > 0.f;
-}
+int pkv_win_tc_heads() { return BM; }
 
 int pkv_launch_win_tc(const PkvWinArgs& a, int64_t Tq, pkv_dtype dt, int D, bool q4, int* launches, void* stream) {
   cudaStream_t s = (cudaStream_t)stream;

@@ -125,9 +125,11 @@ int pkv_launch_append(const PkvAppendArgs& a, pkv_dtype dt, bool q4, void* strea
 int pkv_launch_gather_q4(const void* kp, const void* vp, int64_t num_blocks, const int32_t* table, int B, int W,
                          int first_block, int n_blocks, void* sk, void* sv, int64_t stage_rows, int Hkv, int D,
                          pkv_dtype dt, unsigned int* err, int check, void* stream);
-int pkv_launch_win_dec(const PkvWinArgs& a, pkv_dtype dt, int D, bool q4, void* stream);
-// tcgen05 path; for calls that pkv_win_tc_supports.
-bool pkv_win_tc_supports(const PkvWinArgs& a, pkv_dtype dt);
+// `ws_wanted` not NULL: nothing is launched, *ws_wanted = the workspace the call would use (0: none).
+int pkv_launch_win_dec(const PkvWinArgs& a, pkv_dtype dt, int D, bool q4, void* workspace, size_t ws_bytes,
+                       size_t* ws_wanted, int* launches, void* stream);
+// tcgen05 path: bf16/f16, a positive scale, at most pkv_win_tc_heads() query heads per kv head.
+int pkv_win_tc_heads();
 int pkv_launch_win_tc(const PkvWinArgs& a, int64_t Tq, pkv_dtype dt, int D, bool q4, int* launches, void* stream);
 int pkv_launch_win_simt(const PkvWinArgs& a, pkv_dtype dt, int D, bool q4, void* stream);
 
@@ -144,6 +146,9 @@ int pkv_prepare_kernel(const void* kernel, int smem, int threads, int regs, PkvK
 int64_t pkv_visible_keys(const PkvWinArgs& a, int64_t tokens);
 // CTAs (1, 2, 4, 8 or 16) that share one item's `steps` key steps; a CTA's set-up and merge cost about `fixed` steps.
 int pkv_plan_cluster(const PkvKernelState& state, int64_t items, int64_t steps, double fixed);
+// Single CTAs (2 .. 64) that share one item where that is estimated under any cluster; else 1.  `combine`: the cost of
+// the launch that merges them, in steps.
+int pkv_plan_splits(const PkvKernelState& state, int64_t items, int64_t steps, double fixed, double combine);
 // The same for a kernel of one CTA per SM: `whole` items run as single CTAs, the others in a second launch of
 // clusters of `ctas` (0 whole items: one launch).
 struct PkvClusterPlan {

@@ -60,11 +60,20 @@ pkv_status append_impl(const char* fn, bool q4, const void* q, int64_t q_stride,
   return PKV_OK;
 }
 
+enum class WinKernel { kSimt, kTc, kDec };
+
+// Up to 32 query rows per kv head the memory-bound kernel, which reads each key once for all of them; beyond, tiles of
+// 256 rows on tcgen05.
+WinKernel win_kernel(pkv_dtype dt, int64_t num_blocks, int64_t max_query_len, int g, uint32_t flags) {
+  if (dt == PKV_F32 || (flags & PKV_FORCE_SIMT)) return WinKernel::kSimt;
+  return max_query_len * g > 32 && num_blocks > 0 && g <= pkv_win_tc_heads() ? WinKernel::kTc : WinKernel::kDec;
+}
+
 pkv_status win_impl(const char* fn, bool q4, const void* q, int64_t Tq, int Hq, const void* key_pool,
                     const void* value_pool, int64_t num_blocks, int block_size, int Hkv, int D, pkv_dtype dt,
                     const int32_t* block_table, int B, int W, const int32_t* query_start_loc, const int32_t* seq_lens,
                     int max_query_len, int max_seq_len, float softmax_scale, int window, int sinks, void* out,
-                    uint32_t flags, void* stream) {
+                    void* workspace, size_t ws_bytes, uint32_t flags, void* stream) {
   pkv_clear_error();
   pkv_set_launches(0);
   if (Tq < 0 || B < 0 || W < 0 || max_query_len < 0 || max_seq_len < 0 || num_blocks < 0)
@@ -92,6 +101,7 @@ pkv_status win_impl(const char* fn, bool q4, const void* q, int64_t Tq, int Hq, 
     return pkv_fail(PKV_ERR_INVALID_ARG, "%s: NULL pointer", fn);
   if (!aligned16(q) || !aligned16(key_pool) || !aligned16(value_pool) || !aligned16(out))
     return pkv_fail(PKV_ERR_INVALID_ARG, "%s: q, pools and out must be 16-byte aligned", fn);
+  if (!aligned16(workspace)) return pkv_fail(PKV_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
   if (num_blocks == 0 && max_seq_len > 0)
     return pkv_fail(PKV_ERR_INVALID_ARG, "%s: keys of up to %d positions in a pool without blocks", fn, max_seq_len);
   PkvWinArgs a{};
@@ -103,16 +113,12 @@ pkv_status win_impl(const char* fn, bool q4, const void* q, int64_t Tq, int Hq, 
   a.scale = softmax_scale;
   a.err = pkv_device_error_word();
   if (!a.err) return pkv_fail(PKV_ERR_CUDA, "%s: device error word unavailable", fn);
-  // Up to 32 query rows per kv head the memory-bound kernel, which reads each key once for all of them; beyond, tiles
-  // of 256 rows on tcgen05.
-  const int64_t rows = (int64_t)max_query_len * (Hq / Hkv);
   int rc, launches = 1;
-  if (dt == PKV_F32 || (flags & PKV_FORCE_SIMT))
-    rc = pkv_launch_win_simt(a, dt, D, q4, stream);
-  else if (rows > 32 && num_blocks > 0 && pkv_win_tc_supports(a, dt))
-    rc = pkv_launch_win_tc(a, Tq, dt, D, q4, &launches, stream);
-  else
-    rc = pkv_launch_win_dec(a, dt, D, q4, stream);
+  switch (win_kernel(dt, num_blocks, max_query_len, Hq / Hkv, flags)) {
+    case WinKernel::kSimt: rc = pkv_launch_win_simt(a, dt, D, q4, stream); break;
+    case WinKernel::kTc: rc = pkv_launch_win_tc(a, Tq, dt, D, q4, &launches, stream); break;
+    default: rc = pkv_launch_win_dec(a, dt, D, q4, workspace, ws_bytes, nullptr, &launches, stream);
+  }
   if (rc) return pkv_fail(PKV_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString((cudaError_t)rc));
   pkv_set_launches(launches);
   return PKV_OK;
@@ -204,6 +210,18 @@ int current_device() {
 
 int pkv_plan_cluster(const PkvKernelState& state, int64_t items, int64_t steps, double fixed) {
   return best_split(state, current_device(), items, steps, fixed).ctas;
+}
+
+int pkv_plan_splits(const PkvKernelState& state, int64_t items, int64_t steps, double fixed, double combine) {
+  const int dev = current_device();
+  const int64_t slots = state.active[dev][0].load(std::memory_order_relaxed);
+  if (slots <= 0 || items * 2 > slots) return 1;
+  int64_t splits = slots / items;
+  if (splits > steps) splits = steps;
+  if (splits > 64) splits = 64;
+  if (splits < 2) return 1;
+  const double cost = (double)((steps + splits - 1) / splits) + fixed + combine;
+  return cost < best_split(state, dev, items, steps, fixed).cost ? (int)splits : 1;
 }
 
 // Whole waves of single CTAs, and a second launch that splits the items behind them, where that is estimated a
@@ -300,23 +318,37 @@ extern "C" pkv_status paged_kv_gather_q4(const void* key_pool, const void* value
   return PKV_OK;
 }
 
+extern "C" size_t paged_attn_window_workspace_size(int64_t num_blocks, int Hq, int Hkv, int D, pkv_dtype dt, int q4, int B,
+                                                   int max_query_len, int max_seq_len, int window, int sinks) {
+  if (num_blocks <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || B <= 0 || max_query_len <= 0 || max_seq_len < 0 ||
+      window < 0 || sinks < 0 || (D != 64 && D != 128) || (int64_t)max_query_len * (Hq / Hkv) > kMaxGrid - 1024 ||
+      (dt != PKV_BF16 && dt != PKV_F16) || win_kernel(dt, num_blocks, max_query_len, Hq / Hkv, 0) != WinKernel::kDec)
+    return 0;
+  PkvWinArgs a{};
+  a.num_blocks = num_blocks, a.B = B, a.Hq = Hq, a.Hkv = Hkv;
+  a.max_query_len = max_query_len, a.max_seq_len = max_seq_len, a.window = window, a.sinks = sinks;
+  size_t bytes = 0;
+  return pkv_launch_win_dec(a, dt, D, q4 != 0, nullptr, 0, &bytes, nullptr, nullptr) == 0 ? bytes : 0;
+}
+
 extern "C" pkv_status paged_attn_window(const void* q, int64_t Tq, int Hq, const void* key_pool,
                                         const void* value_pool, int64_t num_blocks, int block_size, int Hkv, int D,
                                         pkv_dtype dt, const int32_t* block_table, int B, int W,
                                         const int32_t* query_start_loc, const int32_t* seq_lens, int max_query_len,
                                         int max_seq_len, float softmax_scale, int window, int sinks, void* out,
-                                        uint32_t flags, void* stream) {
+                                        void* workspace, size_t ws_bytes, uint32_t flags, void* stream) {
   return win_impl("paged_attn_window", false, q, Tq, Hq, key_pool, value_pool, num_blocks, block_size, Hkv, D, dt,
                   block_table, B, W, query_start_loc, seq_lens, max_query_len, max_seq_len, softmax_scale, window,
-                  sinks, out, flags, stream);
+                  sinks, out, workspace, ws_bytes, flags, stream);
 }
 
 extern "C" pkv_status paged_attn_q4(const void* q, int64_t Tq, int Hq, const void* key_pool, const void* value_pool,
                                     int64_t num_blocks, int block_size, int Hkv, int D, pkv_dtype dt,
                                     const int32_t* block_table, int B, int W, const int32_t* query_start_loc,
                                     const int32_t* seq_lens, int max_query_len, int max_seq_len, float softmax_scale,
-                                    int window, int sinks, void* out, uint32_t flags, void* stream) {
+                                    int window, int sinks, void* out, void* workspace,
+                                    size_t ws_bytes, uint32_t flags, void* stream) {
   return win_impl("paged_attn_q4", true, q, Tq, Hq, key_pool, value_pool, num_blocks, block_size, Hkv, D, dt,
                   block_table, B, W, query_start_loc, seq_lens, max_query_len, max_seq_len, softmax_scale, window,
-                  sinks, out, flags, stream);
+                  sinks, out, workspace, ws_bytes, flags, stream);
 }

@@ -179,7 +179,7 @@ def test_gather_q4_flags_bad_blocks(lib):
 
 
 def attention(lib, rows, hq, hkv, d, dtype, window, sinks, q4=False, seed=0, flags=0, scale=None, poison=True, tail=0,
-              table_pad=0):
+              table_pad=0, workspace=None):
     """Run one call; returns (got, want, tolerance).  What no query sees is NaN, its blocks are not listed."""
     g = torch.Generator().manual_seed(seed)
     lens = [r[1] for r in rows]
@@ -220,7 +220,7 @@ def attention(lib, rows, hq, hkv, d, dtype, window, sinks, q4=False, seed=0, fla
     fn = lib.paged_attn_q4 if q4 else lib.paged_attn_window
     fn(q.cuda(), kp.cuda(), vp.cuda(), torch.from_numpy(table).cuda(), torch.from_numpy(qsl).cuda(),
        torch.tensor(lens, dtype=torch.int32).cuda(), max(1, max(r[0] for r in rows)), max(lens), scale, window=window,
-       sinks=sinks, out=out, flags=flags | lib.PKV_CHECK_BOUNDS)
+       sinks=sinks, out=out, workspace=workspace, flags=flags | lib.PKV_CHECK_BOUNDS)
     assert lib.check() == 0 and lib.last_launches() in (1, 2)
     out = out.double().cpu().numpy()
     assert (out[qsl[-1]:] == 77).all()
@@ -429,3 +429,46 @@ def test_repeated_calls_give_the_same_bits(lib, q4):
 ])
 def test_prompt_tiles(lib, rows, hq, hkv, d, window, sinks, dtype, q4):
     agree(*attention(lib, rows, hq, hkv, d, dtype, window, sinks, q4, seed=hq + len(rows), tail=3))
+
+
+@pytest.mark.parametrize("q4,dtype", [(False, "bf16"), (True, "bf16"), (True, "f16")])
+@pytest.mark.parametrize("rows,hq,hkv,d,window,sinks", [
+    ([(1, 9000)], 8, 1, 128, 0, 0),
+    ([(1, 5000), (1, 0), (2, 700)], 4, 2, 64, 1500, 40),
+    ([(1, 9000), (1, 0), (2, 700)], 4, 2, 64, 7500, 40),
+    ([(3, 5500)], 5, 1, 128, 0, 0),       # 15 rows
+    ([(4, 6500), (1, 33)], 7, 1, 64, 5900, 1),  # 28 rows
+])
+def test_few_sequences_share_keys(lib, rows, hq, hkv, d, window, sinks, q4, dtype):
+    """CTAs of one tile merge through a workspace (the caller's, the binding's) or, without one, in clusters."""
+    size = lib.window_workspace_size(10 ** 4, hq, hkv, d, sc.DT[dtype], len(rows), max(r[0] for r in rows),
+                                     max(r[1] for r in rows), window, sinks, q4)
+    if not size:  # so few steps that a cluster is quicker than a second launch
+        assert rows[0][1] <= 5000 and len(rows) == 3
+        agree(*attention(lib, rows, hq, hkv, d, dtype, window, sinks, q4, seed=4, tail=2))
+        assert lib.last_launches() == 1
+        return
+    assert size % 16 == 0
+    for ws in (None, torch.full((size,), 255, dtype=torch.uint8, device="cuda"), torch.empty(0, device="cuda"),
+               torch.empty(size - 16, dtype=torch.uint8, device="cuda")):
+        got = attention(lib, rows, hq, hkv, d, dtype, window, sinks, q4, seed=4, workspace=ws, tail=2)
+        assert lib.last_launches() == (2 if ws is None or ws.numel() >= size else 1)
+        agree(*got)
+
+
+def test_shared_keys_on_another_stream(lib):
+    """The binding's own scratch belongs to the stream of the call."""
+    g = torch.Generator().manual_seed(0)
+    pool = torch.randn(4096, 1, 64, generator=g).bfloat16().cuda()
+    q = torch.randn(1, 4, 64, generator=g).bfloat16().cuda()
+    meta = (torch.arange(256, dtype=torch.int32)[None].cuda(), torch.tensor([0, 1], dtype=torch.int32).cuda(),
+            torch.tensor([4096], dtype=torch.int32).cuda())
+    want = lib.paged_attn_window(q, pool, pool, *meta, 1, 4096, 0.1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [torch.empty_like(q) for _ in range(20)]
+    for out in outs:
+        lib.paged_attn_window(q, pool, pool, *meta, 1, 4096, 0.1, out=out, stream=side)
+        torch.full((1 << 16,), 3.0, device="cuda")  # would land in scratch freed too early
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)

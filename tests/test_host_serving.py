@@ -45,9 +45,10 @@ def test_append_of_nothing_is_a_no_op(name):
 
 
 def attn(name="paged_attn_window", q=P, Tq=4, hq=4, kp=P, vp=P, nblk=8, bs=16, hkv=2, d=64, dt=lib.PKV_BF16, table=P,
-         B=1, W=2, qsl=P, lens=P, mq=4, ml=32, scale=0.125, window=0, sinks=0, out=P, flags=0):
+         B=1, W=2, qsl=P, lens=P, mq=4, ml=32, scale=0.125, window=0, sinks=0, out=P, ws=None, nws=0,
+         flags=0):
     return getattr(lib.lib, name)(q, Tq, hq, kp, vp, nblk, bs, hkv, d, dt, table, B, W, qsl, lens, mq, ml, scale,
-                                  window, sinks, out, flags, None)
+                                  window, sinks, out, ws, nws, flags, None)
 
 
 @pytest.mark.parametrize("name", ["paged_attn_window", "paged_attn_q4"])
@@ -65,6 +66,7 @@ def attn(name="paged_attn_window", q=P, Tq=4, hq=4, kp=P, vp=P, nblk=8, bs=16, h
     (dict(ml=33), lib.PKV_ERR_INVALID_ARG, "max_seq_len"),
     (dict(table=None), lib.PKV_ERR_INVALID_ARG, "NULL"),
     (dict(out=P + 2), lib.PKV_ERR_INVALID_ARG, "aligned"),
+    (dict(ws=P + 8), lib.PKV_ERR_INVALID_ARG, "workspace"),
     (dict(nblk=0), lib.PKV_ERR_INVALID_ARG, "without blocks"),
     (dict(mq=2 ** 31 - 1), lib.PKV_ERR_UNSUPPORTED, "too many"),
 ])
