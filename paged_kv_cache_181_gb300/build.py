@@ -26,7 +26,8 @@ LIB = os.path.join(PKG, "libpagedkv.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_SOURCES = ["device.cu", "kv_write.cu", "attn_simt.cu", "attn_tc.cu", "noalloc.cu", "selftest.cu", "serving.cu",
-                "kv_append.cu", "attn_win_simt.cu", "attn_win_dec.cu", "attn_win_tc.cu"]
+                "kv_append.cu", "attn_win_simt.cu", "attn_win_dec.cu", "attn_q4_dec.cu",
+                "attn_win_tc.cu"]
 HOST_SOURCES = ["host.cpp"]
 
 
@@ -68,7 +69,7 @@ REGISTER_GATES = (
 # Sources whose ptxas report is kept beside their object (`<source>.ptxas.txt`): the tensor-core kernel's for
 # the gate below, the CUDA-core kernel's for its spill check (it runs at 252-254 registers, where a
 # toolchain that allocated differently would start spilling: slower, not wrong), and the window kernels' for both.
-PTXAS_LOGGED = (TC_SOURCE, "attn_simt.cu", "attn_win_tc.cu", "attn_win_dec.cu")
+PTXAS_LOGGED = (TC_SOURCE, "attn_simt.cu", "attn_win_tc.cu", "attn_win_dec.cu", "attn_q4_dec.cu")
 
 
 def expected_tc_registers(source: str, name: str = "kLaunchRegs") -> int:

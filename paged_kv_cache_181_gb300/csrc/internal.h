@@ -126,8 +126,10 @@ int pkv_launch_gather_q4(const void* kp, const void* vp, int64_t num_blocks, con
                          int first_block, int n_blocks, void* sk, void* sv, int64_t stage_rows, int Hkv, int D,
                          pkv_dtype dt, unsigned int* err, int check, void* stream);
 // `ws_wanted` not NULL: nothing is launched, *ws_wanted = the workspace the call would use (0: none).
-int pkv_launch_win_dec(const PkvWinArgs& a, pkv_dtype dt, int D, bool q4, void* workspace, size_t ws_bytes,
-                       size_t* ws_wanted, int* launches, void* stream);
+int pkv_launch_win_dec(const PkvWinArgs& a, pkv_dtype dt, int D, void* ws, size_t ws_bytes, size_t* ws_wanted,
+                       int* launches, void* stream);
+int pkv_launch_q4_dec(const PkvWinArgs& a, pkv_dtype dt, int D, void* ws, size_t ws_bytes, size_t* ws_wanted,
+                      int* launches, void* stream);
 // tcgen05 path: bf16/f16, a positive scale, at most pkv_win_tc_heads() query heads per kv head.
 int pkv_win_tc_heads();
 int pkv_launch_win_tc(const PkvWinArgs& a, int64_t Tq, pkv_dtype dt, int D, bool q4, int* launches, void* stream);

@@ -117,7 +117,8 @@ pkv_status win_impl(const char* fn, bool q4, const void* q, int64_t Tq, int Hq, 
   switch (win_kernel(dt, num_blocks, max_query_len, Hq / Hkv, flags)) {
     case WinKernel::kSimt: rc = pkv_launch_win_simt(a, dt, D, q4, stream); break;
     case WinKernel::kTc: rc = pkv_launch_win_tc(a, Tq, dt, D, q4, &launches, stream); break;
-    default: rc = pkv_launch_win_dec(a, dt, D, q4, workspace, ws_bytes, nullptr, &launches, stream);
+    default:
+      rc = (q4 ? pkv_launch_q4_dec : pkv_launch_win_dec)(a, dt, D, workspace, ws_bytes, nullptr, &launches, stream);
   }
   if (rc) return pkv_fail(PKV_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString((cudaError_t)rc));
   pkv_set_launches(launches);
@@ -328,7 +329,7 @@ extern "C" size_t paged_attn_window_workspace_size(int64_t num_blocks, int Hq, i
   a.num_blocks = num_blocks, a.B = B, a.Hq = Hq, a.Hkv = Hkv;
   a.max_query_len = max_query_len, a.max_seq_len = max_seq_len, a.window = window, a.sinks = sinks;
   size_t bytes = 0;
-  return pkv_launch_win_dec(a, dt, D, q4 != 0, nullptr, 0, &bytes, nullptr, nullptr) == 0 ? bytes : 0;
+  return (q4 ? pkv_launch_q4_dec : pkv_launch_win_dec)(a, dt, D, nullptr, 0, &bytes, nullptr, nullptr) == 0 ? bytes : 0;
 }
 
 extern "C" pkv_status paged_attn_window(const void* q, int64_t Tq, int Hq, const void* key_pool,
