@@ -4,7 +4,7 @@
 // into operands weigh as much as the memory.
 //
 // A page's records (K and V, 1280 contiguous bytes each for D = 128) come by one bulk copy each into a ring of the
-// warp's own, RING pages deep, so no register waits for memory and the loop holds no addresses.  Codes become
+// warp's own, four pages deep, so no register waits for memory and the loop holds no addresses.  Codes become
 // fp16(step * n + low), exactly the value the format gives them, in 13 instructions per 8 of them (q4.cuh).  Both products
 // run in fp16; Q is scaled per row by a power of two into fp16's range (exact for all but values 2^-24 of the row's
 // largest), and the scores scaled back in fp32.
@@ -19,8 +19,8 @@ namespace {
 
 using namespace dec;
 
-constexpr int kRing = 4;   // pages in flight or in use per warp
-constexpr int kPG = 2;     // pages per step
+constexpr int kPG = 2;    // pages per step
+constexpr int kRing = 2;  // steps in flight or in use per warp
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
 PKV_DEVINLINE uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -119,7 +119,7 @@ PKV_DEVINLINE int chan(int g, int e, int c) { return D == 128 ? 16 * g + 8 * c +
 template <int D, int NT>
 struct Smem {
   union {
-    uint8_t ring[kWarps][kRing][2][Q4<D>::kRecord];
+    uint8_t ring[kWarps][kRing][kPG][2][Q4<D>::kRecord];
     MergeSmem<D, NT> merge;
   };
   uint64_t full[kWarps][kRing];
@@ -156,20 +156,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
   }
   if (tid == 0) sm.abort = 0;
   __syncwarp();
-  auto issue = [&](int i) {  // page i into its slot of the ring; i counts up by one from call to call
+  // Pages i .. i + kPG - 1 into step slot (i / kPG) % kRing, a lane per record; i counts up by kPG from call to call.
+  const uint8_t* const pool = (const uint8_t*)((lane & 1) ? a.v_pool : a.k_pool) + (int64_t)pl.kvh * Q4<D>::kRecord;
+  auto issue = [&](int i) {
     if (i >= n) return;
     if (i && (i & 31) == 0) ids = ids_next, ids_next = fetch_ids(i + 32);
-    const int blk = __shfl_sync(0xffffffffu, ids, i & 31);
-    if (lane == 0) {
-      const int s = i % kRing;
-      const int64_t at = ((int64_t)blk * a.Hkv + pl.kvh) * Q4<D>::kRecord;
-      ptx::mbar_arrive_expect_tx(&sm.full[warp][s], 2 * Q4<D>::kRecord);
-      bulk_load(sm.ring[warp][s][0], (const uint8_t*)a.k_pool + at, Q4<D>::kRecord, &sm.full[warp][s]);
-      bulk_load(sm.ring[warp][s][1], (const uint8_t*)a.v_pool + at, Q4<D>::kRecord, &sm.full[warp][s]);
-    }
+    const int blk = __shfl_sync(0xffffffffu, ids, (i + (lane >> 1)) & 31);
+    const int pages = n - i < kPG ? n - i : kPG;
+    const int slot = (i / kPG) % kRing;
+    if (lane == 0) ptx::mbar_arrive_expect_tx(&sm.full[warp][slot], 2 * pages * Q4<D>::kRecord);
+    __syncwarp();
+    if (lane < 2 * pages)
+      bulk_load(sm.ring[warp][slot][lane >> 1][lane & 1], pool + (int64_t)blk * (a.Hkv * Q4<D>::kRecord), Q4<D>::kRecord,
+                &sm.full[warp][slot]);
   };
 #pragma unroll
-  for (int i = 0; i < kRing; ++i) issue(i);
+  for (int i = 0; i < kRing; ++i) issue(i * kPG);
 
   // Q operands: n = query row gl of each group of eight, channels in the order that q4_unpack gives.
   uint4 q[QS ? 1 : NT][D / 32];
@@ -219,56 +221,55 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
   State<D, NT> st;
   st.clear();
   const int key = key_of(gl);
+  // Pages [v_lo, v_hi) of the list hold keys that every row sees (besides whole sink pages, which take the masked way).
+  int v_lo = 0, v_hi = p_first + 1 > 0 ? (p_first + 1) >> 4 : 0;  // as logical pages
+  if (a.window && p_last - (a.window - 1) > 0) v_lo = (p_last - (a.window - 1) + 15) >> 4;
+  v_lo += pg.n_sink - pg.first, v_hi += pg.n_sink - pg.first;
+  if (v_lo < pg.n_sink) v_lo = pg.n_sink;
   for (int i = 0; i < n; i += kPG) {
-    int j0[kPG];
-    unsigned seen[kPG];
-    bool all = true, ok = true;
-#pragma unroll
-    for (int u = 0; u < kPG; ++u) {
-      const bool there = i + u < n;
-      j0[u] = there ? pg.page(gw + (i + u) * stride) * 16 : 0x3ffffff0;
-      all = all && j0[u] + 15 <= p_first && (a.window == 0 || j0[u] + 15 < a.sinks || p_last - j0[u] < a.window);
-      // Keys that some row sees: every key of a page that `all` rows see, else one by one.
-      seen[u] = all ? 0xffffu : __ballot_sync(0xffffffffu, pg.any(j0[u] + (lane & 15))) & 0xffffu;
-      if (there)
-        ok = ok && ptx::mbar_wait(&sm.full[warp][(i + u) % kRing], ((i + u) / kRing) & 1, &sm.abort, kWaitLimitNs);
-    }
-    if (!__all_sync(0xffffffffu, ok)) {
+    const int v = gw + i * stride, slot = (i / kPG) % kRing;
+    const bool all = v >= v_lo && v + (kPG - 1) * stride < v_hi;  // v_hi <= pg.n: every page of the step is there
+    if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sm.full[warp][slot], (i / (kPG * kRing)) & 1, &sm.abort, kWaitLimitNs))) {
       sm.abort = 1;
       if (lane == 0) pkv_raise(a.err, PKV_DEVERR_TIMEOUT);
       break;
     }
+    unsigned seen[kPG];
     float s[kPG][NT][4] = {};
 #pragma unroll
     for (int u = 0; u < kPG; ++u)
-      k_steps<D>(sm.ring[warp][(i + u) % kRing][0], gl, tl, [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+      k_steps<D>(sm.ring[warp][slot][u][0], gl, tl, [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint4 qq = QS ? sm.q[nt][k >> 1][lane] : q[QS ? 0 : nt][k >> 1];
           mma<false>(s[u][nt], a0, a1, a2, a3, (k & 1) ? qq.z : qq.x, (k & 1) ? qq.w : qq.y);
         }
       });
+#pragma unroll
+    for (int u = 0; u < kPG; ++u) seen[u] = 0xffffu;
     if (!all) {
 #pragma unroll
-      for (int u = 0; u < kPG; ++u)
+      for (int u = 0; u < kPG; ++u) {
+        const int j0 = i + u < n ? pg.page(v + u * stride) * 16 : 0x3ffffff0;
+        seen[u] = __ballot_sync(0xffffffffu, pg.any(j0 + (lane & 15))) & 0xffffu;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            s[u][nt][c] = win_sees(p[nt][c & 1], j0[u] + key + 8 * (c >> 1), a.window, a.sinks) ? s[u][nt][c] : -INFINITY;
+            s[u][nt][c] = win_sees(p[nt][c & 1], j0 + key + 8 * (c >> 1), a.window, a.sinks) ? s[u][nt][c] : -INFINITY;
+      }
     }
     uint32_t b0[kPG][NT], b1[kPG][NT];
     st.template update<false>(s, f, b0, b1);
 #pragma unroll
     for (int u = 0; u < kPG; ++u)
-      v_tiles<D>(sm.ring[warp][(i + u) % kRing][1], gl, tl, seen[u],
+      v_tiles<D>(sm.ring[warp][slot][u][1], gl, tl, seen[u],
                  [&](int e, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
                    for (int nt = 0; nt < NT; ++nt) mma<false>(st.o[nt][e], a0, a1, a2, a3, b0[u][nt], b1[u][nt]);
                  });
     __syncwarp();  // every lane has read the step's pages
-#pragma unroll
-    for (int u = 0; u < kPG; ++u) issue(i + kRing + u);
+    issue(i + kRing * kPG);
   }
   if (sm.abort && lane == 0) {
     // Let copies already issued land before the shared memory goes away.

@@ -20,17 +20,20 @@ struct Q4 {
 // Eight codes of one word (channel i at bits 4i) as fp16 pairs: h[i] = (n_i, n_{i+4}), exact.
 // 0x6400 is 1024 in fp16, whose last bit is worth 1: or-ing a nibble into the low bits gives 1024 + n, and one
 // four bits higher 1024 + 16 n.
+PKV_DEVINLINE __half2 q4_pick(uint32_t w, uint32_t mask) {
+  // (w & mask) | 0x64006400 in one instruction: with both constants as immediates it would be two.
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(0x64006400u));
+  return *reinterpret_cast<__half2*>(&d);
+}
 PKV_DEVINLINE void q4_unpack(uint32_t w, __half2 (&h)[4]) {
-  const uint32_t magic = 0x64006400u;
-  const uint32_t x0 = (w & 0x000f000fu) | magic, x1 = (w & 0x00f000f0u) | magic;
-  w >>= 8;
-  const uint32_t x2 = (w & 0x000f000fu) | magic, x3 = (w & 0x00f000f0u) | magic;
   const __half2 k1024 = __half2half2(__ushort_as_half(0x6400));
   const __half2 sixteenth = __half2half2(__ushort_as_half(0x2c00)), k64 = __half2half2(__ushort_as_half(0xd400));  // 1/16, -64
-  h[0] = __hsub2(*reinterpret_cast<const __half2*>(&x0), k1024);
-  h[1] = __hfma2(*reinterpret_cast<const __half2*>(&x1), sixteenth, k64);
-  h[2] = __hsub2(*reinterpret_cast<const __half2*>(&x2), k1024);
-  h[3] = __hfma2(*reinterpret_cast<const __half2*>(&x3), sixteenth, k64);
+  h[0] = __hsub2(q4_pick(w, 0x000f000fu), k1024);
+  h[1] = __hfma2(q4_pick(w, 0x00f000f0u), sixteenth, k64);
+  w >>= 8;
+  h[2] = __hsub2(q4_pick(w, 0x000f000fu), k1024);
+  h[3] = __hfma2(q4_pick(w, 0x00f000f0u), sixteenth, k64);
 }
 
 // The eight fp16 values of a word under one pair, as h[i] = (value_i, value_{i+4}).

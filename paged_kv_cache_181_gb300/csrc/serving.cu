@@ -185,7 +185,7 @@ struct Split {
   double cost;
 };
 
-// A launch runs in waves of the clusters that fit the GPU at once; each CTA takes its share of the steps plus the
+// A kernel of one CTA per SM runs in waves of the clusters that fit the GPU at once; each CTA takes its share of the steps plus the
 // fixed cost.  The smallest estimate wins, a larger cluster only where it gains a tenth.
 Split best_split(const PkvKernelState& state, int dev, int64_t items, int64_t steps, double fixed) {
   Split best{1, 1e300};
@@ -209,8 +209,28 @@ int current_device() {
 
 }  // namespace
 
+// Kernels of several CTAs per SM share its rate, so a launch takes about its whole work over the CTAs that run at
+// once, and, at the end, half a CTA's time more while they run out.
+static double shared_cost(int64_t ctas, int64_t at_once, int64_t steps, double fixed) {
+  const double one = (double)steps + fixed, waves = (double)ctas / (double)at_once;
+  return (waves > 1.0 ? waves : 1.0) * one + 0.5 * one;
+}
+
+static Split best_cluster(const PkvKernelState& state, int dev, int64_t items, int64_t steps, double fixed) {
+  Split best{1, 1e300};
+  for (int i = 0; i < 5; ++i) {
+    const int c = 1 << i;
+    const int64_t active = state.active[dev][i].load(std::memory_order_relaxed);
+    if (active <= 0 && c > 1) break;
+    if (c > 1 && (steps < 2 * c || items * c > kMaxGrid)) break;
+    const double cost = shared_cost(items * c, (active > 0 ? active : 152) * c, (steps + c - 1) / c, fixed);
+    if (cost < 0.97 * best.cost) best = Split{c, cost};
+  }
+  return best;
+}
+
 int pkv_plan_cluster(const PkvKernelState& state, int64_t items, int64_t steps, double fixed) {
-  return best_split(state, current_device(), items, steps, fixed).ctas;
+  return best_cluster(state, current_device(), items, steps, fixed).ctas;
 }
 
 int pkv_plan_splits(const PkvKernelState& state, int64_t items, int64_t steps, double fixed, double combine) {
@@ -219,10 +239,14 @@ int pkv_plan_splits(const PkvKernelState& state, int64_t items, int64_t steps, d
   if (slots <= 0 || items * 2 > slots) return 1;
   int64_t splits = slots / items;
   if (splits > steps) splits = steps;
-  if (splits > 64) splits = 64;
+  if (splits > 64) {
+    // As many CTAs on every SM.
+    const int64_t sms = pkv_sm_count() > 0 ? pkv_sm_count() : 152;
+    splits = items * 64 >= sms ? items * 64 / sms * sms / items : 64;
+  }
   if (splits < 2) return 1;
-  const double cost = (double)((steps + splits - 1) / splits) + fixed + combine;
-  return cost < best_split(state, dev, items, steps, fixed).cost ? (int)splits : 1;
+  const double cost = shared_cost(items * splits, slots, (steps + splits - 1) / splits, fixed) + combine;
+  return cost < best_cluster(state, dev, items, steps, fixed).cost ? (int)splits : 1;
 }
 
 // Whole waves of single CTAs, and a second launch that splits the items behind them, where that is estimated a

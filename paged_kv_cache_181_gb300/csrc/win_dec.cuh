@@ -12,6 +12,8 @@ namespace dec {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr float kRescale = 8.f;  // log2 units
+// What a CTA's set-up and merge, and a combine launch, take in steps (one page per warp).
+constexpr double kFixedSteps = 3.0, kCombineSteps = 2.0;
 
 template <bool BF16>
 PKV_DEVINLINE void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -276,7 +278,7 @@ int launch(Kernel kernel, PkvKernelState& state, size_t smem, const PkvWinArgs& 
   const int64_t items = (int64_t)a.B * a.Hkv * (((int64_t)a.max_query_len * g + 8 * NT - 1) / (8 * NT));
   const int64_t steps = pkv_visible_keys(a, 8 * NT / g + 1) / (16 * kWarps) + 1;
   // Items too few for clusters of 16 to fill the GPU: more CTAs per item, and the combine launch.
-  int splits = pkv_plan_splits(state, items, steps, 4.0, 3.0);
+  int splits = pkv_plan_splits(state, items, steps, kFixedSteps, kCombineSteps);
   const size_t need = splits > 1 ? (size_t)(items * splits * kPartialFloats<D, NT> * 4) : 0;
   if (ws_wanted) {
     *ws_wanted = need;
@@ -285,7 +287,7 @@ int launch(Kernel kernel, PkvKernelState& state, size_t smem, const PkvWinArgs& 
   if (need > ws_bytes || !workspace) splits = 1;
   float* ws = splits > 1 ? (float*)workspace : nullptr;
   void* args[] = {const_cast<PkvWinArgs*>(&a), &splits, &ws};
-  const int ctas = splits > 1 ? 1 : pkv_plan_cluster(state, items, steps, 4.0);
+  const int ctas = splits > 1 ? 1 : pkv_plan_cluster(state, items, steps, kFixedSteps);
   *launches = 1;
   rc = pkv_launch_cluster((const void*)kernel, splits > 1 ? items * splits : items, ctas, kThreads, smem, args, false, s);
   if (rc || splits == 1) return rc;
