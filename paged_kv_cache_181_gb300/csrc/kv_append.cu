@@ -4,10 +4,14 @@
 // All three are bound by memory: the append reads (Hq + 2 Hkv) D values a token and writes as many (Q and K rotated,
 // V as it is), with about one operation per byte.
 //
-// One thread produces one vector of 8 channels of one head.  A rotated channel needs its partner (rot_dim/2 away,
-// or its neighbour): the thread loads both vectors; the partner's bytes are another lane's own, in the same warp
-// (a head is D/8 = 8 or 16 lanes), so they come from L1.  In fp32: two products and one sum, each rounded, so that
-// results do not depend on how a compiler contracts them.
+// A thread takes two vectors of 8 channels that the rotation pairs (rot_dim/2 apart) or, where it does not, two
+// others, and keeps their cosines and sines in registers while it walks over the heads of its token, loading four
+// heads' vectors before it uses the first.  In fp32: two products and one sum, each rounded, so that results do not
+// depend on how a compiler contracts them.
+//
+// 4-bit pools: the four lanes that hold a group of 32 channels in one of their two vectors find its range with two
+// shuffles each.  The pairs of vectors keep groups on four neighbouring lanes for every rot_dim that is a multiple of
+// 64; any other takes a kernel with one vector a thread, which loads its partner's vector as well.
 
 #include "q4.cuh"
 
@@ -94,6 +98,141 @@ PKV_DEVINLINE void store_q4(unsigned mask, uint8_t* record, int token, int vec, 
   }
 }
 
+// A vector of 8 channels as it lies in memory.
+template <typename T>
+struct Raw {
+  uint4 w[sizeof(T) / 2];
+  PKV_DEVINLINE void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  PKV_DEVINLINE void get(float (&x)[8]) const {
+    const T* e = reinterpret_cast<const T*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = pkv_to_f32<T>(e[i]);
+  }
+};
+
+// Block: as many tokens as its threads hold groups of D/16 * HG; of a token's HG groups of D/16 threads each walks every
+// HG-th head.
+template <typename T, int D, bool Q4POOL, int HG>
+__global__ void __launch_bounds__(kThreads) append_pairs_kernel(const PkvAppendArgs a) {
+  constexpr int U = D / 16, NH = sizeof(T) == 4 ? 2 : 4;
+  const int64_t t = (int64_t)blockIdx.x * (blockDim.x / (U * HG)) + threadIdx.x / (U * HG);
+  const int u = threadIdx.x % U, hg = threadIdx.x / U % HG;
+  if (t >= a.T) return;  // whole groups of four lanes, and the shuffles below stay inside them
+  const int64_t slot = a.slots[t];
+  const int heads = a.Hq + 2 * a.Hkv, half = a.rot_dim / 2;
+  int64_t pos = 0;
+  if (a.rot_dim) {
+    pos = a.positions[t];
+    if (a.check && (pos < 0 || pos >= a.max_position)) {
+      if (u == 0 && hg == 0) pkv_raise(a.err, PKV_DEVERR_POSITION);
+      return;
+    }
+  }
+  int stop = heads;  // a token without a slot has Q heads only
+  if (slot < 0) stop = a.Hq;
+  if (a.check && slot >= a.num_slots) {
+    if (u == 0 && hg == 0) pkv_raise(a.err, PKV_DEVERR_SLOT);
+    stop = a.Hq;
+  }
+  // The thread's vectors, v0 and v1, of rotated heads (Q, K), and w0, w1 of V heads.
+  const int w0 = Q4POOL || a.interleaved ? (u & ~3) * 2 + (u & 3) : 2 * u, w1 = Q4POOL || a.interleaved ? w0 + 4 : w0 + 1;
+  int v0 = w0, v1 = w1;
+  const bool paired = !a.interleaved && u < a.rot_dim / 16;
+  if (!a.interleaved) {
+    if (paired) {
+      v0 = u, v1 = u + a.rot_dim / 16;
+    } else {
+      const int k = u - a.rot_dim / 16;  // behind the rotated channels
+      v0 = a.rot_dim / 8 + (Q4POOL ? (k & ~3) * 2 + (k & 3) : 2 * k);
+      v1 = v0 + (Q4POOL ? 4 : 1);
+    }
+  }
+  float cc[8], ss[8];
+  const float* row = a.cos_sin + pos * a.rot_dim;
+  if (paired) {
+    load8<float>(row + 8 * u, cc);
+    load8<float>(row + half + 8 * u, ss);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float4 c = make_float4(1.f, 1.f, 1.f, 1.f), z = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int v = k ? v1 : v0;
+      if (a.interleaved && 8 * v < a.rot_dim) {
+        c = *reinterpret_cast<const float4*>(row + 4 * v);
+        z = *reinterpret_cast<const float4*>(row + half + 4 * v);
+      }
+      cc[4 * k] = c.x, cc[4 * k + 1] = c.y, cc[4 * k + 2] = c.z, cc[4 * k + 3] = c.w;
+      ss[4 * k] = z.x, ss[4 * k + 1] = z.y, ss[4 * k + 2] = z.z, ss[4 * k + 3] = z.w;
+    }
+  }
+  const bool turn0 = a.interleaved && 8 * v0 < a.rot_dim, turn1 = a.interleaved && 8 * v1 < a.rot_dim;
+  const T* const q = (const T*)a.q + t * a.q_stride;
+  const T* const k = (const T*)a.k + t * a.k_stride;
+  const T* const v = (const T*)a.v + t * a.v_stride;
+  for (int h0 = hg; h0 < stop; h0 += NH * HG) {
+    Raw<T> r0[NH], r1[NH];
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      const int h = h0 + i * HG;
+      if (h < stop) {
+        const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
+        const T* src = is_q ? q + (int64_t)h * D : is_v ? v + (int64_t)(h - a.Hq - a.Hkv) * D : k + (int64_t)(h - a.Hq) * D;
+        r0[i].load(src + 8 * (is_v ? w0 : v0));
+        r1[i].load(src + 8 * (is_v ? w1 : v1));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      const int h = h0 + i * HG;
+      if (h >= stop) break;
+      const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
+      float x[8], y[8];
+      r0[i].get(x);
+      r1[i].get(y);
+      if (!is_v) {
+        if (paired) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float xe = x[e];
+            x[e] = __fsub_rn(__fmul_rn(xe, cc[e]), __fmul_rn(y[e], ss[e]));
+            y[e] = __fadd_rn(__fmul_rn(y[e], cc[e]), __fmul_rn(xe, ss[e]));
+          }
+        } else if (a.interleaved) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float xa = x[2 * e], xb = x[2 * e + 1], ya = y[2 * e], yb = y[2 * e + 1];
+            if (turn0) {
+              x[2 * e] = __fsub_rn(__fmul_rn(xa, cc[e]), __fmul_rn(xb, ss[e]));
+              x[2 * e + 1] = __fadd_rn(__fmul_rn(xb, cc[e]), __fmul_rn(xa, ss[e]));
+            }
+            if (turn1) {
+              y[2 * e] = __fsub_rn(__fmul_rn(ya, cc[4 + e]), __fmul_rn(yb, ss[4 + e]));
+              y[2 * e + 1] = __fadd_rn(__fmul_rn(yb, cc[4 + e]), __fmul_rn(ya, ss[4 + e]));
+            }
+          }
+        }
+      }
+      const int o0 = is_v ? w0 : v0, o1 = is_v ? w1 : v1;
+      if (Q4POOL && !is_q) {
+        const int hk = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
+        uint8_t* record = (uint8_t*)(is_v ? a.v_pool : a.k_pool) + ((slot >> 4) * a.Hkv + hk) * Q4<D>::kRecord;
+        const unsigned mask = 0xfu << (threadIdx.x & 28);  // the four lanes of a group share its head
+        store_q4<D>(mask, record, (int)(slot & 15), o0, x);
+        store_q4<D>(mask, record, (int)(slot & 15), o1, y);
+      } else {
+        T* dst = is_q ? (T*)a.q_out + (t * a.Hq + h) * D
+                      : (T*)(is_v ? a.v_pool : a.k_pool) + (slot * a.Hkv + (is_v ? h - a.Hq - a.Hkv : h - a.Hq)) * D;
+        store8<T>(dst + 8 * o0, x);
+        store8<T>(dst + 8 * o1, y);
+      }
+    }
+  }
+}
+
+// One vector a thread: 4-bit pools with a rot_dim that splits groups over more than four lanes.
 // Grid: x = token, y = groups of kThreads / (D/8) heads (Q heads, then K, then V).
 template <typename T, int D, bool Q4POOL>
 __global__ void __launch_bounds__(kThreads) append_kernel(const PkvAppendArgs a) {
@@ -171,51 +310,79 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const PkvAppendArgs a)
   }
 }
 
-// stage[b][first*16 + i] = the values of token i of the listed blocks.  One thread per 8 channels.
+// stage[b][first*16 + i] = the values of token i of the listed blocks.  Grid: x = listed block, y = (row, K|V); a thread
+// takes 8 channels at a time, several in flight, in the order of the staging rows.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
     gather_q4_kernel(const uint8_t* __restrict__ kp, const uint8_t* __restrict__ vp, int64_t num_blocks,
-                     const int32_t* __restrict__ table, int W, int first_block, int n_blocks, T* __restrict__ sk,
-                     T* __restrict__ sv, int64_t stage_rows, int Hkv, int64_t n, unsigned int* err, int check) {
-  constexpr int VECS = D / 8;
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < n; u += (int64_t)gridDim.x * kThreads) {
-    const int vec = (int)(u % VECS);
-    int64_t r = u / VECS;
-    const int h = (int)(r % Hkv);
-    r /= Hkv;
-    const int token = (int)(r & 15);
-    r >>= 4;
-    const int page = (int)(r % n_blocks);
-    r /= n_blocks;
-    const bool is_v = r & 1;
-    const int64_t b = r >> 1;
-    const int blk = __ldg(table + b * W + first_block + page);
-    if (check && (blk < 0 || blk >= num_blocks)) {
-      if (token == 0 && vec == 0 && h == 0) pkv_raise(err, PKV_DEVERR_BLOCK);
-      continue;
-    }
-    const uint8_t* rec = (is_v ? vp : kp) + ((int64_t)blk * Hkv + h) * Q4<D>::kRecord;
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(rec + token * Q4<D>::kRowBytes) + vec);
-    const __half2 pair = __ldg(reinterpret_cast<const __half2*>(rec + Q4<D>::kPairs) + token * Q4<D>::kGroups + (vec >> 2));
-    __half2 hv[4];
-    q4_values(w, pair, hv);
-    float x[8];
+                     const int32_t* __restrict__ table, int W, int first_block, T* __restrict__ sk, T* __restrict__ sv,
+                     int64_t stage_rows, int Hkv, unsigned int* err, int check) {
+  constexpr int VECS = D / 8, NU = 4;
+  const int b = blockIdx.y >> 1, page = first_block + blockIdx.x;
+  const bool is_v = blockIdx.y & 1;
+  const int blk = __ldg(table + (int64_t)b * W + page);
+  if (check && (blk < 0 || blk >= num_blocks)) {
+    if (threadIdx.x == 0) pkv_raise(err, PKV_DEVERR_BLOCK);
+    return;
+  }
+  const uint8_t* recs = (is_v ? vp : kp) + (int64_t)blk * Hkv * Q4<D>::kRecord;
+  T* dst = (is_v ? sv : sk) + (b * stage_rows + (int64_t)page * 16) * Hkv * D;
+  const int per_token = Hkv * VECS, n = 16 * per_token;
+  for (int e0 = threadIdx.x; e0 < n; e0 += NU * kThreads) {
+    uint32_t w[NU];
+    __half2 pair[NU];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __low2float(hv[i]), x[i + 4] = __high2float(hv[i]);
-    const int64_t row = b * stage_rows + (int64_t)(first_block + page) * 16 + token;
-    store8<T>((is_v ? sv : sk) + (row * Hkv + h) * D + vec * 8, x);
+    for (int i = 0; i < NU; ++i) {
+      const int e = e0 + i * kThreads;
+      if (e < n) {
+        const int token = e / per_token, r = e - token * per_token, h = r / VECS, vec = r % VECS;
+        const uint8_t* rec = recs + (int64_t)h * Q4<D>::kRecord;
+        w[i] = __ldg(reinterpret_cast<const uint32_t*>(rec + token * Q4<D>::kRowBytes) + vec);
+        pair[i] = __ldg(reinterpret_cast<const __half2*>(rec + Q4<D>::kPairs) + token * Q4<D>::kGroups + (vec >> 2));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int e = e0 + i * kThreads;
+      if (e < n) {
+        __half2 hv[4];
+        q4_values(w[i], pair[i], hv);
+        float x[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = __low2float(hv[c]), x[c + 4] = __high2float(hv[c]);
+        store8<T>(dst + (int64_t)e * 8, x);
+      }
+    }
   }
 }
 
-template <typename T, int D>
-int launch_append(const PkvAppendArgs& a, bool q4, cudaStream_t s) {
-  constexpr int per = kThreads / (D / 8);
-  const dim3 grid((unsigned)a.T, (unsigned)((a.Hq + 2 * a.Hkv + per - 1) / per));
-  if (q4)
-    append_kernel<T, D, true><<<grid, kThreads, 0, s>>>(a);
-  else
-    append_kernel<T, D, false><<<grid, kThreads, 0, s>>>(a);
+template <typename T, int D, bool Q4POOL>
+int launch_append(const PkvAppendArgs& a, cudaStream_t s) {
+  if (Q4POOL && !a.interleaved && a.rot_dim % 64) {
+    constexpr int per = kThreads / (D / 8);
+    const dim3 grid((unsigned)a.T, (unsigned)((a.Hq + 2 * a.Hkv + per - 1) / per));
+    append_kernel<T, D, Q4POOL><<<grid, kThreads, 0, s>>>(a);
+    return (int)cudaGetLastError();
+  }
+  // Few tokens: a block per token, four heads a thread at most while they last.  Many: several tokens a block, and more
+  // heads to a thread's cosines and sines.
+  constexpr int U = D / 16;
+  if (a.T < 1024) {
+    if (a.Hq + 2 * a.Hkv > 32)
+      append_pairs_kernel<T, D, Q4POOL, 16><<<(unsigned)a.T, U * 16, 0, s>>>(a);
+    else
+      append_pairs_kernel<T, D, Q4POOL, 8><<<(unsigned)a.T, U * 8, 0, s>>>(a);
+  } else {
+    constexpr int PER = kThreads / (U * 8);
+    append_pairs_kernel<T, D, Q4POOL, 8><<<(unsigned)((a.T + PER - 1) / PER), kThreads, 0, s>>>(a);
+  }
   return (int)cudaGetLastError();
+}
+
+template <typename T>
+int launch_append_t(const PkvAppendArgs& a, bool q4, cudaStream_t s) {
+  if (q4) return a.D == 64 ? launch_append<T, 64, true>(a, s) : launch_append<T, 128, true>(a, s);
+  return a.D == 64 ? launch_append<T, 64, false>(a, s) : launch_append<T, 128, false>(a, s);
 }
 
 }  // namespace
@@ -223,10 +390,9 @@ int launch_append(const PkvAppendArgs& a, bool q4, cudaStream_t s) {
 int pkv_launch_append(const PkvAppendArgs& a, pkv_dtype dt, bool q4, void* stream) {
   cudaStream_t s = (cudaStream_t)stream;
   switch (dt) {
-    case PKV_F32: return a.D == 64 ? launch_append<float, 64>(a, q4, s) : launch_append<float, 128>(a, q4, s);
-    case PKV_BF16:
-      return a.D == 64 ? launch_append<__nv_bfloat16, 64>(a, q4, s) : launch_append<__nv_bfloat16, 128>(a, q4, s);
-    case PKV_F16: return a.D == 64 ? launch_append<__half, 64>(a, q4, s) : launch_append<__half, 128>(a, q4, s);
+    case PKV_F32: return launch_append_t<float>(a, q4, s);
+    case PKV_BF16: return launch_append_t<__nv_bfloat16>(a, q4, s);
+    case PKV_F16: return launch_append_t<__half>(a, q4, s);
   }
   return (int)cudaErrorInvalidValue;
 }
@@ -236,14 +402,13 @@ template <typename T, int D>
 int launch_gather(const void* kp, const void* vp, int64_t num_blocks, const int32_t* table, int B, int W,
                   int first_block, int n_blocks, void* sk, void* sv, int64_t stage_rows, int Hkv, unsigned int* err,
                   int check, cudaStream_t s) {
-  int sms = pkv_sm_count();
-  if (sms <= 0) sms = 152;
-  const int64_t n = (int64_t)B * 2 * n_blocks * 16 * Hkv * (D / 8);
-  int64_t grid = (n + kThreads - 1) / kThreads;
-  if (grid > (int64_t)sms * 32) grid = (int64_t)sms * 32;
-  gather_q4_kernel<T, D><<<(unsigned)grid, kThreads, 0, s>>>((const uint8_t*)kp, (const uint8_t*)vp, num_blocks, table,
-                                                             W, first_block, n_blocks, (T*)sk, (T*)sv, stage_rows, Hkv,
-                                                             n, err, check);
+  for (int b0 = 0; b0 < B; b0 += 32767) {  // a grid's y extent
+    const int nb = B - b0 < 32767 ? B - b0 : 32767;
+    const int64_t at = (int64_t)b0 * stage_rows * Hkv * D;
+    gather_q4_kernel<T, D><<<dim3((unsigned)n_blocks, (unsigned)(2 * nb)), kThreads, 0, s>>>(
+        (const uint8_t*)kp, (const uint8_t*)vp, num_blocks, table + (int64_t)b0 * W, W, first_block, (T*)sk + at,
+        (T*)sv + at, stage_rows, Hkv, err, check);
+  }
   return (int)cudaGetLastError();
 }
 }  // namespace
