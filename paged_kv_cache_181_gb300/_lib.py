@@ -404,17 +404,20 @@ def q4_block_bytes(head_dim: int) -> int:
 
 
 # These calls are a few microseconds of GPU time in a decode step, so their argument checks are written for few
-# interpreter steps: one pass over the tensors, the raw stream handle, no temporary objects.  (Through the helpers
-# above a call took 18 us of host time.)
+# interpreter steps: one expression over the tensors, the raw stream handle, no temporary objects.  (Through the
+# helpers above a call took 18 us of host time.)
 _DTYPES: dict = {}
-_raw_stream = _current_device = None
+_raw_stream = _current_device = _u8 = _i32t = _i64 = _f32 = None
 
 
 def _init_fast() -> None:
-    global _raw_stream, _current_device
+    global _raw_stream, _current_device, _u8, _i32t, _i64, _f32
     torch = _torch()
+    _u8, _i32t, _i64, _f32 = torch.uint8, torch.int32, torch.int64, torch.float32
     _DTYPES.update({torch.float32: PKV_F32, torch.bfloat16: PKV_BF16, torch.float16: PKV_F16})
     _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    if not torch.cuda.is_available():
+        _current_device = lambda: -2  # noqa: E731  (no tensor is on it)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
@@ -428,19 +431,18 @@ def _code(fn: str, dtype) -> int:
     return c
 
 
-def _check_device(fn: str, tensors) -> int:
-    """Every tensor contiguous and on the current CUDA device; returns the device's index."""
-    dev = tensors[0].get_device()
+def _refuse_placement(fn: str, *tensors) -> None:
+    """Say what is wrong with tensors that are not all contiguous and on the current CUDA device."""
     for t in tensors:
-        if t.get_device() != dev or not t.is_contiguous() or dev < 0:
-            if not t.is_cuda:
-                raise ValueError(f"{fn}: tensors must be on a CUDA device (got {t.device})")
-            if not t.is_contiguous():
-                raise ValueError(f"{fn}: tensors must be contiguous")
-            raise ValueError(f"{fn}: tensors must be on one CUDA device (got {tensors[0].device} and {t.device})")
-    if dev != _current_device():
-        raise ValueError(f"{fn}: tensors are on cuda:{dev}, the current device is cuda:{_current_device()}")
-    return dev
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{fn}: tensors must be on a CUDA device (got {t.device})")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: tensors must be contiguous")
+        if t.get_device() != _current_device():
+            raise ValueError(f"{fn}: tensors must be on one CUDA device, the current one: cuda:{_current_device()} "
+                             f"(got {t.device})")
 
 
 def _token_stride(fn: str, name: str, x) -> int:
@@ -454,9 +456,10 @@ def _token_stride(fn: str, name: str, x) -> int:
 
 def _append(fn: str, entry, q4: bool, q, k, v, positions, cos_sin, slot_mapping, key_pool, value_pool, interleaved,
             q_out, flags, stream):
-    torch = _torch()
     shape, dtype = k.shape, k.dtype
-    code = _code(fn, dtype)
+    code = _DTYPES.get(dtype)
+    if code is None:
+        code = _code(fn, dtype)
     if len(shape) != 3 or v.shape != shape:
         raise ValueError(f"{fn}: k and v must be [T, Hkv, D]")
     T, hkv, d = shape
@@ -466,43 +469,49 @@ def _append(fn: str, entry, q4: bool, q, k, v, positions, cos_sin, slot_mapping,
     pool_shape = key_pool.shape
     if len(pool_shape) != 3 or value_pool.shape != pool_shape:
         raise ValueError(f"{fn}: the pools must be 3-D and of one shape")
-    tensors = [key_pool, value_pool, slot_mapping]
     if q is not None:
         q_shape = q.shape
         if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != d:
             raise ValueError(f"{fn}: q must be [T, Hq, D]")
         hq = q_shape[1]
         if q_out is None:
-            q_out = torch.empty(q_shape, dtype=q.dtype, device=q.device)
+            q_out = _torch().empty(q_shape, dtype=q.dtype, device=q.device)
         elif q_out.shape != q_shape:
             raise ValueError(f"{fn}: q_out shape {tuple(q_out.shape)} differs from q {tuple(q_shape)}")
         if q.dtype != dtype or q_out.dtype != dtype:
             raise ValueError(f"{fn}: q, k, v and q_out must share one dtype")
         q_at, q_stride, q_out_at = q.data_ptr(), _token_stride(fn, "q", q), q_out.data_ptr()
-        tensors.append(q_out)
     elif q_out is not None:
         raise ValueError(f"{fn}: q_out given without q")
     _, pool_heads, width = pool_shape
     if pool_heads != hkv or width != (10 * d if q4 else d):
         raise ValueError(f"{fn}: the pools must be [{'num_blocks' if q4 else 'num_slots'}, {hkv}, {10 * d if q4 else d}]")
-    pool_dtype = torch.uint8 if q4 else dtype
+    pool_dtype = _u8 if q4 else dtype
     if key_pool.dtype != pool_dtype or value_pool.dtype != pool_dtype:
         raise ValueError(f"{fn}: 4-bit pools are uint8" if q4 else f"{fn}: sources and pools must share one dtype")
-    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
+    if slot_mapping.dtype != _i64 or slot_mapping.numel() != T:
         raise ValueError(f"{fn}: slot_mapping must be int64 [T]")
     rot = max_position = pos_at = cs_at = 0
     if cos_sin is not None:
-        if positions is None or positions.dtype != torch.int32 or positions.numel() != T:
+        if positions is None or positions.dtype != _i32t or positions.numel() != T:
             raise ValueError(f"{fn}: positions must be int32 [T]")
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        if cos_sin.dtype != _f32 or cos_sin.dim() != 2:
             raise ValueError(f"{fn}: cos_sin must be float32 [max_position, rot_dim]")
         max_position, rot = cos_sin.shape
         if rot:
             pos_at, cs_at = positions.data_ptr(), cos_sin.data_ptr()
-            tensors += (positions, cos_sin)
-    dev = _check_device(fn, tensors)
-    if k.get_device() != dev or v.get_device() != dev or (hq and q.get_device() != dev):
-        raise ValueError(f"{fn}: tensors must be on one CUDA device")
+    dev = _current_device()
+    if not (k.get_device() == v.get_device() == key_pool.get_device() == value_pool.get_device()
+            == slot_mapping.get_device() == dev and key_pool.is_contiguous() and value_pool.is_contiguous()
+            and slot_mapping.is_contiguous()):
+        _refuse_placement(fn, key_pool, value_pool, slot_mapping)
+        raise ValueError(f"{fn}: tensors must be on one CUDA device (got {k.device} and {v.device})")
+    if q is not None and not (q.get_device() == q_out.get_device() == dev and q_out.is_contiguous()):
+        _refuse_placement(fn, q_out)
+        raise ValueError(f"{fn}: tensors must be on one CUDA device (got {q.device})")
+    if rot and not (positions.get_device() == cos_sin.get_device() == dev and positions.is_contiguous()
+                    and cos_sin.is_contiguous()):
+        _refuse_placement(fn, positions, cos_sin)
     status = entry(q_at, q_stride, k.data_ptr(), _token_stride(fn, "k", k), v.data_ptr(), _token_stride(fn, "v", v),
                    pos_at, cs_at, max_position, rot, slot_mapping.data_ptr(), T, hq, q_out_at, key_pool.data_ptr(),
                    value_pool.data_ptr(), pool_shape[0], hkv, d, code,
@@ -534,7 +543,7 @@ def paged_kv_append_q4(q, k, v, positions, cos_sin, slot_mapping, key_pool, valu
 def paged_kv_gather_q4(key_pool, value_pool, block_table, stage_k, stage_v, *, first_block: int = 0,
                        n_blocks: int | None = None, flags: int = 0, stream=None) -> None:
     """The values of table blocks [first_block, first_block + n_blocks) of every row, into ``stage_k/v [B, rows, Hkv, D]``."""
-    fn, torch = "paged_kv_gather_q4", _torch()
+    fn = "paged_kv_gather_q4"
     code = _code(fn, stage_k.dtype)
     shape, pool_shape = stage_k.shape, key_pool.shape
     if block_table.dim() != 2 or len(shape) != 4 or len(pool_shape) != 3:
@@ -547,11 +556,15 @@ def paged_kv_gather_q4(key_pool, value_pool, block_table, stage_k, stage_v, *, f
         raise ValueError(f"{fn}: staging buffers must be [B, rows, Hkv, D], of one dtype")
     if value_pool.shape != pool_shape or pool_shape[1] != hkv or pool_shape[2] != 10 * d:
         raise ValueError(f"{fn}: the pools must be [num_blocks, {hkv}, {10 * d}]")
-    if key_pool.dtype != torch.uint8 or value_pool.dtype != torch.uint8:
+    if key_pool.dtype != _u8 or value_pool.dtype != _u8:
         raise ValueError(f"{fn}: 4-bit pools are uint8")
-    if block_table.dtype != torch.int32:
+    if block_table.dtype != _i32t:
         raise ValueError(f"{fn}: block_table must be int32")
-    dev = _check_device(fn, (key_pool, value_pool, block_table, stage_k, stage_v))
+    dev = _current_device()
+    if not (key_pool.get_device() == value_pool.get_device() == block_table.get_device() == stage_k.get_device()
+            == stage_v.get_device() == dev and key_pool.is_contiguous() and value_pool.is_contiguous()
+            and block_table.is_contiguous() and stage_k.is_contiguous() and stage_v.is_contiguous()):
+        _refuse_placement(fn, key_pool, value_pool, block_table, stage_k, stage_v)
     status = lib.paged_kv_gather_q4(key_pool.data_ptr(), value_pool.data_ptr(), pool_shape[0], block_table.data_ptr(),
                                     B, W, int(first_block), int(n_blocks), stage_k.data_ptr(), stage_v.data_ptr(), rows,
                                     hkv, d, code, flags, _raw_stream(dev) if stream is None else stream.cuda_stream)
@@ -561,9 +574,10 @@ def paged_kv_gather_q4(key_pool, value_pool, block_table, stage_k, stage_v, *, f
 
 def _attn_window(fn: str, entry, q4: bool, q, key_pool, value_pool, block_table, query_start_loc, seq_lens,
                  max_query_len, max_seq_len, softmax_scale, window, sinks, out, workspace, flags, block_size, stream):
-    torch = _torch()
     shape, dtype, pool_shape, table_shape = q.shape, q.dtype, key_pool.shape, block_table.shape
-    code = _code(fn, dtype)
+    code = _DTYPES.get(dtype)
+    if code is None:
+        code = _code(fn, dtype)
     if len(shape) != 3 or len(pool_shape) != 3 or len(table_shape) != 2:
         raise ValueError(f"{fn}: q must be [Tq, Hq, D], the pools 3-D and block_table [B, W]")
     Tq, hq, d = shape
@@ -574,13 +588,13 @@ def _attn_window(fn: str, entry, q4: bool, q, key_pool, value_pool, block_table,
     if q4:
         if width != 10 * d:
             raise ValueError(f"{fn}: the pools must be [num_blocks, Hkv, {10 * d}]")
-        pool_dtype = torch.uint8
+        pool_dtype = _u8
     else:
         if width != d or block_size <= 0 or blocks % block_size:
             raise ValueError(f"{fn}: the pools must be [num_blocks * {block_size}, Hkv, {d}]")
         blocks, pool_dtype = blocks // block_size, dtype
     if out is None:
-        out = torch.empty_like(q)
+        out = _torch().empty_like(q)
     elif out.shape != shape:
         raise ValueError(f"{fn}: out shape {tuple(out.shape)} differs from q {tuple(shape)}")
     if query_start_loc.numel() != B + 1 or seq_lens.numel() != B:
@@ -588,19 +602,25 @@ def _attn_window(fn: str, entry, q4: bool, q, key_pool, value_pool, block_table,
                          f"(got {query_start_loc.numel()} and {seq_lens.numel()})")
     if key_pool.dtype != pool_dtype or value_pool.dtype != pool_dtype or out.dtype != dtype:
         raise ValueError(f"{fn}: the pools must be {pool_dtype} and out of q's dtype")
-    i32 = torch.int32
-    if block_table.dtype != i32 or query_start_loc.dtype != i32 or seq_lens.dtype != i32:
+    if block_table.dtype != _i32t or query_start_loc.dtype != _i32t or seq_lens.dtype != _i32t:
         raise ValueError(f"{fn}: metadata must be int32")
-    dev = _check_device(fn, (q, key_pool, value_pool, block_table, query_start_loc, seq_lens, out))
+    dev = _current_device()
+    if not (q.get_device() == key_pool.get_device() == value_pool.get_device() == block_table.get_device()
+            == query_start_loc.get_device() == seq_lens.get_device() == out.get_device() == dev and q.is_contiguous()
+            and key_pool.is_contiguous() and value_pool.is_contiguous() and block_table.is_contiguous()
+            and query_start_loc.is_contiguous() and seq_lens.is_contiguous() and out.is_contiguous()):
+        _refuse_placement(fn, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, out)
     ws_at = ws_bytes = 0
     if workspace is not None:
-        _check_device(fn, (q, workspace))
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _refuse_placement(fn, workspace)
         ws_at, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    elif B * hkv < 256 and code:  # more items than that never take one
+    elif B * hkv < 256 and code and max_seq_len > 1024 and (window > 1024 or window == 0):
+        # Few sequences and heads over many keys (no other sizes take a workspace).
         ws_bytes = lib.paged_attn_window_workspace_size(blocks, hq, hkv, d, code, q4, B, max_query_len, max_seq_len,
                                                         window, sinks)
         if ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            workspace = _torch().empty(ws_bytes, dtype=_u8, device=q.device)
             ws_at = workspace.data_ptr()
             if stream is not None:
                 workspace.record_stream(stream)

@@ -236,7 +236,7 @@ int pkv_plan_cluster(const PkvKernelState& state, int64_t items, int64_t steps, 
 int pkv_plan_splits(const PkvKernelState& state, int64_t items, int64_t steps, double fixed, double combine) {
   const int dev = current_device();
   const int64_t slots = state.active[dev][0].load(std::memory_order_relaxed);
-  if (slots <= 0 || items * 2 > slots) return 1;
+  if (slots <= 0 || items * 2 > slots || steps <= 16) return 1;  // (up to 1024 keys a cluster has a step per CTA)
   int64_t splits = slots / items;
   if (splits > steps) splits = steps;
   if (splits > 64) {
