@@ -118,38 +118,54 @@ PKV_DEVINLINE void store_pair<float>(float* p, float x, float y) {
 }
 
 // Each CTA holds, for every row of the tile, the sum o[row][D] of exp2(x - m[row]) v over its keys, m and l (the sum
-// of the exponentials); m is in log2 units and -inf when it saw no key.  The CTAs of the cluster write the merged
-// rows, each its share of the channel pairs.  Ends with a cluster barrier: no CTA leaves while another reads it.
+// of the exponentials); m is in log2 units and -inf when it saw no key.  The rows are dealt out over the cluster's
+// warps: a lane fetches one CTA's m and l, then D/32 channels of every CTA, so that the remote reads (some 0.2 us each)
+// overlap.  Ends with a cluster barrier: no CTA leaves while another reads it.  o_stride is even.
 template <typename T, int D>
 PKV_DEVINLINE void win_merge_store(const float* o, int o_stride, const float* m, const float* l, int rows, int r0, int g,
                                    int kvh, int Hq, int q0, T* out, int tid, int threads) {
+  constexpr int CH = D / 32;
   const uint32_t rank = cluster_rank(), n = cluster_size();
+  __syncwarp();
   if (n > 1)
     cluster_sync();
   else
     __syncthreads();
-  const int pairs = rows * (D / 2);
-  for (int e = rank * threads + tid; e < pairs; e += n * threads) {
-    const int r = e / (D / 2), c = (e % (D / 2)) * 2;
-    float x = 0.f, y = 0.f, sum = 0.f;
+  const int warp = tid >> 5, lane = tid & 31, warps = threads >> 5;
+  for (int r = rank * warps + warp; r < rows; r += n * warps) {
+    float acc[CH] = {}, sum = 0.f;
     if (n == 1) {
-      x = o[r * o_stride + c], y = o[r * o_stride + c + 1], sum = l[r];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) acc[c] = o[r * o_stride + lane * CH + c];
+      sum = l[r];
     } else {
-      float top = -INFINITY;
-      for (uint32_t k = 0; k < n; ++k) top = fmaxf(top, cluster_ld(cluster_addr(m + r, k)));
+      float mk = -INFINITY, lk = 0.f;
+      if (lane < (int)n) mk = cluster_ld(cluster_addr(m + r, lane)), lk = cluster_ld(cluster_addr(l + r, lane));
+      float top = mk;
+#pragma unroll
+      for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+      const float w = mk == top ? 1.f : exp2f(mk - top);  // CTAs without keys hold zeros
+#pragma unroll 8
       for (uint32_t k = 0; k < n; ++k) {
-        const float mk = cluster_ld(cluster_addr(m + r, k));
-        if (mk == -INFINITY && cluster_ld(cluster_addr(l + r, k)) == 0.f) continue;
-        const float w = mk == top ? 1.f : exp2f(mk - top);
-        sum += w * cluster_ld(cluster_addr(l + r, k));
-        const float2 v = cluster_ld2(cluster_addr(o + r * o_stride + c, k));
-        x += w * v.x, y += w * v.y;
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const uint32_t src = cluster_addr(o + r * o_stride + lane * CH, k);
+#pragma unroll
+        for (int c = 0; c < CH; c += 2) {
+          const float2 x = cluster_ld2(src + c * 4);
+          acc[c] += wk * x.x, acc[c + 1] += wk * x.y;
+        }
+        sum += wk * __shfl_sync(0xffffffffu, lk, k);
       }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a NaN sum stays
     const int row = r0 + r;
     const int64_t tok = (int64_t)q0 + row / g;
-    store_pair<T>(out + (tok * Hq + kvh * g + row % g) * D + c, x * inv, y * inv);
+    T* dst = out + (tok * Hq + kvh * g + row % g) * D + lane * CH;
+#pragma unroll
+    for (int c = 0; c < CH; c += 2) store_pair<T>(dst + c, acc[c] * inv, acc[c + 1] * inv);
   }
-  if (n > 1) cluster_sync();
+  if (n > 1) {
+    __syncwarp();
+    cluster_sync();
+  }
 }

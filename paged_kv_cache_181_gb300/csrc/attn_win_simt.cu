@@ -1,10 +1,17 @@
 // Window/sinks attention on the CUDA cores, every type of pool: fp32 arithmetic throughout.
 //
-// One cluster = 32 packed query rows (attn_win.cuh) of one (sequence, kv head); its CTAs take the 32-key tiles in
-// turn and merge at the end.  A CTA has 4 warps of 8 rows: scores with a lane per key (K rows padded by 16 bytes, so
-// the lanes' float4 reads spread over the banks; Q rows are broadcast reads), an online softmax with the
-// running maximum and sum in registers, then P.V with a lane per D/32 channels.  This is the path of fp32 calls
-// (tensor cores have no fp32 product) and of PKV_FORCE_SIMT.
+// One cluster = a tile of packed query rows (attn_win.cuh) of one (sequence, kv head); its CTAs take the keys in turn and
+// merge at the end.  This is the path of fp32 calls (tensor cores have no fp32 product) and of PKV_FORCE_SIMT.
+//
+// Tiles of 32 rows: a CTA's 4 warps have 8 rows each and share tiles of 32 keys in shared memory.  Scores with a lane
+// per key (K rows padded by 16 bytes, so the lanes' float4 reads spread over the banks; Q rows are broadcast reads), an
+// online softmax with the running maximum and sum in registers, then P.V with a lane per D/32 channels.  16 warps an SM
+// hide what each waits for; tiles of 64 keys, two a lane, and register tiles of 8 x 4 scores need fewer reads for an FMA
+// but leave 8 warps, and measured slower (3 sequences, 333 queries, window 501: 72 and 90 us instead of 51).
+
+// Calls of at most 8 rows (decode): bound by memory, so keys and values go from memory to registers.  Half a warp
+// takes a key, a lane D/16 of its channels for every row; four keys at a time, whose scores are summed over the half
+// warp by four shuffles each; each half warp has a softmax state of its own until the end.
 
 #include <atomic>
 
@@ -15,9 +22,9 @@
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRows = 32;  // query rows per CTA
-constexpr int kKeys = 32;  // keys per tile
-constexpr int kWarpRows = kRows / 4;
+constexpr int kWarps = kThreads / 32;
+constexpr int kWarpRows = 8;  // query rows of a warp
+constexpr int kRows = kWarps * kWarpRows, kKeys = 32;  // of a CTA's tile
 
 struct PoolQ4 {};
 
@@ -25,9 +32,18 @@ template <int D>
 struct Smem {
   float q[kRows][D];
   float k[kKeys][D + 4];
-  float v[kKeys][D];
+  float v[kKeys][D];  // at the end, the rows' sums
   float p[kRows][kKeys];
   float m[kRows], l[kRows];
+};
+
+template <int D>
+struct FewSmem {
+  static constexpr int kStates = 2 * kWarps;  // a half warp's each
+  static constexpr int kStride = D + 4;
+  float o[kStates][kWarpRows][kStride];
+  float wm[kStates][kWarpRows], wl[kStates][kWarpRows];
+  float m[kWarpRows], l[kWarpRows];
 };
 
 // CH channels [c, c + CH) of key `slot` (pool row) of head kvh, as fp32.
@@ -36,7 +52,10 @@ struct Loader {
   static PKV_DEVINLINE void load(const void* pool, int64_t blk, int token, int Hkv, int kvh, int c, float (&x)[CH]) {
     const T* p = (const T*)pool + ((blk * 16 + token) * Hkv + kvh) * D + c;
     alignas(16) T v[CH];
-    if constexpr (CH * sizeof(T) == 16)
+    if constexpr (CH * sizeof(T) == 32)
+      reinterpret_cast<uint4*>(v)[0] = reinterpret_cast<const uint4*>(p)[0],
+      reinterpret_cast<uint4*>(v)[1] = reinterpret_cast<const uint4*>(p)[1];
+    else if constexpr (CH * sizeof(T) == 16)
       *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
     else if constexpr (CH * sizeof(T) == 8)
       *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
@@ -172,22 +191,137 @@ __global__ void __launch_bounds__(kThreads) attn_win_simt_kernel(const PkvWinArg
 }
 
 template <typename T, typename Pool, int D>
-int launch(const PkvWinArgs& a, cudaStream_t s) {
-  auto kernel = attn_win_simt_kernel<T, Pool, D>;
-  const size_t smem = sizeof(Smem<D>);
-  static PkvKernelState state;
+__global__ void __launch_bounds__(kThreads, 2) attn_win_simt_few_kernel(const PkvWinArgs a) {
+  constexpr int CH = D / 16, U = 4;  // channels of a lane; keys of a half warp per step
+  using S = FewSmem<D>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  S& sm = *reinterpret_cast<S*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = lane >> 4, c0 = (lane & 15) * CH;
+  const int g = a.Hq / a.Hkv;
+  const uint32_t rank = cluster_rank(), n_cta = cluster_size();
+  const uint32_t item = blockIdx.x / n_cta;
+  const int kvh = item % a.Hkv, b = item / a.Hkv;
+  const WinRow row = win_row(a, b, tid == 0 && kvh == 0 && rank == 0);
+  const int rows = row.Sq * g;
+  if (rows <= 0) return;  // the whole cluster leaves
+  const int base = row.L - row.Sq;
+  const WinPages pg = win_pages(base, base + row.Sq - 1, a.window, a.sinks);
+  const float sl2 = a.scale * 1.4426950408889634f;
+  float q[kWarpRows][CH], o[kWarpRows][CH] = {}, m[kWarpRows], l[kWarpRows] = {};
+#pragma unroll
+  for (int r = 0; r < kWarpRows; ++r) {
+    m[r] = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      q[r][c] = 0.f;
+      if (r < rows)
+        q[r][c] = pkv_to_f32<T>(((const T*)a.q)[(((int64_t)row.q0 + r / g) * a.Hq + kvh * g + r % g) * D + c0 + c]) * sl2;
+    }
+  }
+  // A warp's step is half a page: keys 8 h .. 8 h + 7, four of them for each half warp.
+  for (int w = rank * kWarps + warp; w < 2 * pg.n; w += n_cta * kWarps) {
+    const int page = pg.page(w >> 1), j0 = page * 16 + (w & 1) * 8 + half * U;
+    const int64_t blk = win_block(a, b, page);
+    float k[U][CH], v[U][CH];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) k[u][c] = v[u][c] = 0.f;
+      if (pg.any(j0 + u)) {
+        Loader<Pool, D, CH>::load(a.k_pool, blk, (j0 + u) & 15, a.Hkv, kvh, c0, k[u]);
+        Loader<Pool, D, CH>::load(a.v_pool, blk, (j0 + u) & 15, a.Hkv, kvh, c0, v[u]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kWarpRows; ++r) {
+      if (r >= rows) break;
+      const int p = base + r / g;
+      float x[U], top = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        x[u] = 0.f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) x[u] = fmaf(q[r][c], k[u][c], x[u]);
+      }
+#pragma unroll
+      for (int d = 8; d; d >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] += __shfl_xor_sync(0xffffffffu, x[u], d);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!win_sees(p, j0 + u, a.window, a.sinks)) x[u] = -INFINITY;
+        top = fmaxf(top, x[u]);
+      }
+      if (top > m[r]) {
+        const float alpha = ptx::ex2(m[r] - top);  // 0 from -inf
+        m[r] = top;
+        l[r] *= alpha;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) o[r][c] *= alpha;
+      }
+      const float mu = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float e = ptx::ex2(x[u] - mu);
+        l[r] += e;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) o[r][c] = fmaf(e, v[u][c], o[r][c]);
+      }
+    }
+  }
+  const int state = warp * 2 + half;
+#pragma unroll
+  for (int r = 0; r < kWarpRows; ++r) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) sm.o[state][r][c0 + c] = o[r][c];
+    if ((lane & 15) == 0) sm.wm[state][r] = m[r], sm.wl[state][r] = l[r];
+  }
+  __syncthreads();
+  for (int e = tid; e < rows * D; e += kThreads) {
+    const int r = e / D, c = e % D;
+    float top = -INFINITY, acc = 0.f, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < S::kStates; ++w) top = fmaxf(top, sm.wm[w][r]);
+#pragma unroll
+    for (int w = 0; w < S::kStates; ++w) {
+      const float f = sm.wm[w][r] == top ? 1.f : ptx::ex2(sm.wm[w][r] - top);
+      acc += f * sm.o[w][r][c];
+      sum += f * sm.wl[w][r];
+    }
+    sm.o[0][r][c] = acc;  // read and written by this thread alone
+    if (c == 0) sm.m[r] = top, sm.l[r] = sum;
+  }
+  win_merge_store<T, D>(&sm.o[0][0][0], S::kStride, sm.m, sm.l, rows, 0, g, kvh, a.Hq, row.q0, (T*)a.out, tid, kThreads);
+}
+
+template <typename Kernel>
+int launch(Kernel kernel, PkvKernelState& state, size_t smem, int64_t items, int64_t steps, double fixed,
+           const PkvWinArgs& a, cudaStream_t s) {
   const int rc = pkv_prepare_kernel((const void*)kernel, (int)smem, kThreads, 0, state);
   if (rc) return rc;
-  const int g = a.Hq / a.Hkv;
-  const int64_t items = (int64_t)a.B * a.Hkv * (((int64_t)a.max_query_len * g + kRows - 1) / kRows);
-  const int ctas = pkv_plan_cluster(state, items, pkv_visible_keys(a, kRows / g + 1) / kKeys + 1, 2.0);
+  const int ctas = pkv_plan_cluster(state, items, steps, fixed);
   void* args[] = {const_cast<PkvWinArgs*>(&a)};
   return pkv_launch_cluster((const void*)kernel, items, ctas, kThreads, smem, args, false, s);
 }
 
+template <typename T, typename Pool, int D>
+int launch_rows(const PkvWinArgs& a, cudaStream_t s) {
+  const int g = a.Hq / a.Hkv;
+  const int64_t rows = (int64_t)a.max_query_len * g;
+  if (rows <= kWarpRows) {
+    static PkvKernelState state;
+    const int64_t keys = pkv_visible_keys(a, a.max_query_len);
+    return launch(attn_win_simt_few_kernel<T, Pool, D>, state, sizeof(FewSmem<D>), (int64_t)a.B * a.Hkv,
+                  keys / (8 * kWarps) + 1, 5.0, a, s);
+  }
+  static PkvKernelState state;
+  return launch(attn_win_simt_kernel<T, Pool, D>, state, sizeof(Smem<D>), (int64_t)a.B * a.Hkv * ((rows + kRows - 1) / kRows),
+                pkv_visible_keys(a, kRows / g + 1) / kKeys + 1, 2.0, a, s);
+}
+
 template <typename T, typename Pool>
 int launch_d(const PkvWinArgs& a, int D, cudaStream_t s) {
-  return D == 64 ? launch<T, Pool, 64>(a, s) : launch<T, Pool, 128>(a, s);
+  return D == 64 ? launch_rows<T, Pool, 64>(a, s) : launch_rows<T, Pool, 128>(a, s);
 }
 
 }  // namespace

@@ -12,8 +12,9 @@ namespace dec {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr float kRescale = 8.f;  // log2 units
-// What a CTA's set-up and merge, and a combine launch, take in steps (one page per warp).
-constexpr double kFixedSteps = 3.0, kCombineSteps = 2.0;
+// What a CTA's set-up and merge take in steps (one page per warp), and what the combine launch has to gain: 3 us on the
+// GPU, and 14 us of the host's time (a workspace, a launch), which a stream of short calls waits for.
+constexpr double kFixedSteps = 3.0, kCombineSteps = 8.0;
 
 template <bool BF16>
 PKV_DEVINLINE void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
