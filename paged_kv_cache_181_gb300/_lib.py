@@ -112,6 +112,12 @@ def _load() -> C.CDLL:
 
 lib = _load()
 
+try:
+    from . import _fastcall
+except ImportError as e:
+    raise ImportError(f"{os.path.join(_HERE, '_fastcall.so')} is not built; run `python -m paged_kv_cache_181_gb300.build` "
+                      f"(or __graft_entry__.build()) first") from e
+
 
 def last_error() -> str:
     return lib.pkv_last_error().decode()
@@ -403,9 +409,9 @@ def q4_block_bytes(head_dim: int) -> int:
     return n
 
 
-# These calls are a few microseconds of GPU time in a decode step, so their argument checks are written for few
-# interpreter steps: one expression over the tensors, the raw stream handle, no temporary objects.  (Through the
-# helpers above a call took 18 us of host time.)
+# These calls are a few microseconds of GPU time in a decode step, so a well-formed one is checked and made by
+# csrc/fastcall.c (4 to 6 us of host time; 18 through the helpers above).  What it does not take -- a wrong argument, a
+# call without q or rotation, a workspace to allocate -- it leaves untouched to the functions here.
 _DTYPES: dict = {}
 _raw_stream = _current_device = _u8 = _i32t = _i64 = _f32 = None
 
@@ -420,6 +426,7 @@ def _init_fast() -> None:
         _current_device = lambda: -2  # noqa: E731  (no tensor is on it)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _fastcall.setup((torch.float32, torch.bfloat16, torch.float16), _u8, _i32t, _i64, _current_device, _raw_stream)
 
 
 def _code(fn: str, dtype) -> int:
@@ -529,6 +536,14 @@ def paged_kv_append(q, k, v, positions, cos_sin, slot_mapping, key_pool, value_p
     q, k and v may be slices of one projection (any token stride); ``q=None`` appends only.  ``cos_sin`` is float32
     ``[max_position, rot_dim]``, cosines then sines; ``None`` rotates nothing.  See include/pagedkv.h.
     """
+    if q_out is None and q is not None:
+        q_out = _torch().empty(q.shape, dtype=q.dtype, device=q.device)
+    status = _fastcall.append(False, q, k, v, positions, cos_sin, slot_mapping, key_pool, value_pool, interleaved, q_out,
+                              flags, stream)
+    if status is not None:
+        if status:
+            _ok(status)
+        return q_out
     return _append("paged_kv_append", lib.paged_kv_append, False, q, k, v, positions, cos_sin, slot_mapping, key_pool,
                    value_pool, interleaved, q_out, flags, stream)
 
@@ -536,6 +551,14 @@ def paged_kv_append(q, k, v, positions, cos_sin, slot_mapping, key_pool, value_p
 def paged_kv_append_q4(q, k, v, positions, cos_sin, slot_mapping, key_pool, value_pool, *, interleaved: bool = False,
                        q_out=None, flags: int = 0, stream=None):
     """paged_kv_append into 4-bit pools (uint8 ``[num_blocks, Hkv, q4_block_bytes(D)]``); returns ``q_out``."""
+    if q_out is None and q is not None:
+        q_out = _torch().empty(q.shape, dtype=q.dtype, device=q.device)
+    status = _fastcall.append(True, q, k, v, positions, cos_sin, slot_mapping, key_pool, value_pool, interleaved, q_out,
+                              flags, stream)
+    if status is not None:
+        if status:
+            _ok(status)
+        return q_out
     return _append("paged_kv_append_q4", lib.paged_kv_append_q4, True, q, k, v, positions, cos_sin, slot_mapping,
                    key_pool, value_pool, interleaved, q_out, flags, stream)
 
@@ -543,6 +566,11 @@ def paged_kv_append_q4(q, k, v, positions, cos_sin, slot_mapping, key_pool, valu
 def paged_kv_gather_q4(key_pool, value_pool, block_table, stage_k, stage_v, *, first_block: int = 0,
                        n_blocks: int | None = None, flags: int = 0, stream=None) -> None:
     """The values of table blocks [first_block, first_block + n_blocks) of every row, into ``stage_k/v [B, rows, Hkv, D]``."""
+    status = _fastcall.gather(key_pool, value_pool, block_table, stage_k, stage_v, first_block, n_blocks, flags, stream)
+    if status is not None:
+        if status:
+            _ok(status)
+        return
     fn = "paged_kv_gather_q4"
     code = _code(fn, stage_k.dtype)
     shape, pool_shape = stage_k.shape, key_pool.shape
@@ -650,6 +678,14 @@ def paged_attn_window(q, key_pool, value_pool, block_table, query_start_loc, seq
     ``workspace`` is scratch of ``window_workspace_size`` bytes that no other call uses at the same time; without one
     the call takes what it needs from torch's allocator.
     """
+    if out is None:
+        out = _torch().empty_like(q)
+    status = _fastcall.attend(False, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len,
+                              max_seq_len, softmax_scale, window, sinks, out, workspace, flags, block_size, stream)
+    if status is not None:
+        if status:
+            _ok(status)
+        return out
     return _attn_window("paged_attn_window", lib.paged_attn_window, False, q, key_pool, value_pool, block_table,
                         query_start_loc, seq_lens, max_query_len, max_seq_len, softmax_scale, window, sinks, out,
                         workspace, flags, block_size, stream)
@@ -659,6 +695,14 @@ def paged_attn_q4(q, key_pool, value_pool, block_table, query_start_loc, seq_len
                   max_seq_len: int, softmax_scale: float, *, window: int = 0, sinks: int = 0, out=None,
                   workspace=None, flags: int = 0, block_size: int = 16, stream=None):
     """paged_attn_window over 4-bit pools (uint8 ``[num_blocks, Hkv, q4_block_bytes(D)]``); returns ``out``."""
+    if out is None:
+        out = _torch().empty_like(q)
+    status = _fastcall.attend(True, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len,
+                              max_seq_len, softmax_scale, window, sinks, out, workspace, flags, block_size, stream)
+    if status is not None:
+        if status:
+            _ok(status)
+        return out
     return _attn_window("paged_attn_q4", lib.paged_attn_q4, True, q, key_pool, value_pool, block_table,
                         query_start_loc, seq_lens, max_query_len, max_seq_len, softmax_scale, window, sinks, out,
                         workspace, flags, block_size, stream)

@@ -16,6 +16,7 @@ import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -29,6 +30,7 @@ CUDA_SOURCES = ["device.cu", "kv_write.cu", "attn_simt.cu", "attn_tc.cu", "noall
                 "kv_append.cu", "attn_win_simt.cu", "attn_win_dec.cu", "attn_q4_dec.cu",
                 "attn_win_tc.cu"]
 HOST_SOURCES = ["host.cpp"]
+FASTCALL = os.path.join(PKG, "_fastcall.so")  # the serving calls' binding, a CPython extension over the library
 
 
 def _nvcc() -> str:
@@ -173,6 +175,12 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
         tmp = LIB + ".tmp"
         _run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs, "-lpthread", "-ldl", "-lrt"], verbose)
         os.replace(tmp, LIB)
+    source = os.path.join(CSRC, "fastcall.c")
+    if force or _stale(FASTCALL, [source, os.path.join(INCLUDE, "pagedkv.h")]):
+        tmp = FASTCALL + ".tmp"
+        _run(["gcc", "-O2", "-shared", "-fPIC", "-Wall", "-I", INCLUDE, "-I", sysconfig.get_path("include"), source, "-o", tmp,
+              "-L", PKG, "-l:libpagedkv.so", "-Wl,-rpath,$ORIGIN"], verbose)
+        os.replace(tmp, FASTCALL)
     return LIB
 
 

@@ -472,3 +472,26 @@ def test_shared_keys_on_another_stream(lib):
         torch.full((1 << 16,), 3.0, device="cuda")  # would land in scratch freed too early
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+def test_ordinary_calls_take_the_fast_way(lib, monkeypatch):
+    def no(*a, **k):
+        raise AssertionError("the careful path ran")
+
+    pool = torch.zeros(64, 2, 64, dtype=torch.bfloat16, device="cuda")
+    four = torch.zeros(4, 2, 640, dtype=torch.uint8, device="cuda")
+    qkv = torch.zeros(3, 8, 64, dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, qsl, lens = torch.zeros(1, 4, **i32), torch.tensor([0, 3], **i32), torch.tensor([20], **i32)
+    pos, slots, cs = torch.arange(3, **i32), torch.arange(3, device="cuda"), torch.zeros(9, 64, device="cuda")
+    lib._code("f", torch.float32)
+    monkeypatch.setattr(lib, "_attn_window", no)
+    monkeypatch.setattr(lib, "_append", no)
+    monkeypatch.setattr(lib, "_refuse_placement", no)
+    q = lib.paged_kv_append(qkv[:, :4], qkv[:, 4:6], qkv[:, 6:], pos, cs, slots, pool, pool)
+    lib.paged_kv_append_q4(qkv[:, :4], qkv[:, 4:6], qkv[:, 6:], pos, cs, slots, four, four, interleaved=True)
+    stage = torch.zeros(1, 64, 2, 64, device="cuda")
+    lib.paged_kv_gather_q4(four, four, table, stage, stage)
+    lib.paged_attn_window(q, pool, pool, table, qsl, lens, 3, 64, 0.1, stream=torch.cuda.current_stream())
+    lib.paged_attn_q4(q, four, four, table, qsl, lens, 3, 64, 0.1, window=4)
+    torch.cuda.synchronize()

@@ -157,3 +157,94 @@ def test_binding_refuses_torn_heads():
         lib._token_stride("f", "q", base)
     assert lib._token_stride("f", "q", torch.zeros(3, 8, 64)[:, 2:6]) == 512
     assert lib._token_stride("f", "q", torch.zeros(1, 8, 64)[:, 2:6]) == 256
+
+
+class FakeTensor:
+    """What csrc/fastcall.c asks of a tensor, without a GPU."""
+
+    def __init__(self, shape, dtype, device=0, contiguous=True, stride=None, at=P):
+        self.shape, self.dtype, self.device, self.contiguous = torch.Size(shape), dtype, device, contiguous
+        self.at = at
+        self.strides = stride or torch.empty(shape, dtype=torch.uint8).stride()
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def data_ptr(self):
+        return self.at
+
+    def stride(self):
+        return self.strides
+
+
+@pytest.fixture
+def fast(monkeypatch):
+    if torch.cuda.is_available():
+        pytest.skip("has a GPU: the addresses here are not memory")
+    from paged_kv_cache_181_gb300 import _fastcall as f
+
+    f.setup((torch.float32, torch.bfloat16, torch.float16), torch.uint8, torch.int32, torch.int64, lambda: 0, lambda d: 0)
+    yield f
+    monkeypatch.setattr(lib, "_DTYPES", {})  # the binding sets it up again with torch's own
+    lib._code("f", torch.float32)
+
+
+def fast_attend(**change):
+    f = FakeTensor
+    a = dict(q4=False, q=f((3, 4, 64), torch.bfloat16), kp=f((32, 2, 64), torch.bfloat16), vp=f((32, 2, 64), torch.bfloat16),
+             table=f((1, 2), torch.int32), qsl=f((2,), torch.int32), lens=f((1,), torch.int32), mq=3, ml=32, scale=0.1,
+             window=0, sinks=0, out=f((3, 4, 64), torch.bfloat16), ws=None, flags=0, bs=16, stream=None)
+    return list((a | change).values())
+
+
+def test_fast_attention_makes_the_call(fast):
+    assert fast.attend(*fast_attend()) == lib.PKV_ERR_CUDA  # it got as far as the device
+    assert fast.attend(*fast_attend(window=-1)) == lib.PKV_ERR_INVALID_ARG and "window" in lib.last_error()
+    four = FakeTensor((2, 2, 640), torch.uint8)
+    assert fast.attend(*fast_attend(q4=True, kp=four, vp=four)) == lib.PKV_ERR_CUDA
+
+
+@pytest.mark.parametrize("change", [
+    dict(q=FakeTensor((3, 4, 64), torch.float64)), dict(q=FakeTensor((3, 4, 64), torch.bfloat16, device=1)),
+    dict(q=FakeTensor((3, 4, 64), torch.bfloat16, device=-1)), dict(kp=FakeTensor((32, 2, 64), torch.float16)),
+    dict(vp=FakeTensor((16, 2, 64), torch.bfloat16)), dict(kp=FakeTensor((30, 2, 64), torch.bfloat16)),
+    dict(table=FakeTensor((1, 2), torch.int64)), dict(table=FakeTensor((2,), torch.int32)),
+    dict(lens=FakeTensor((2,), torch.int32)), dict(qsl=FakeTensor((3,), torch.int32)),
+    dict(out=FakeTensor((3, 4, 32), torch.bfloat16)), dict(out=FakeTensor((3, 4, 64), torch.bfloat16, contiguous=False)),
+    dict(ws=FakeTensor((64,), torch.uint8)), dict(bs=32), dict(mq=2.0), dict(mq=2 ** 40), dict(scale="x"), dict(q4=True),
+    dict(q=None), dict(stream=7), dict(flags=None),
+])
+def test_fast_attention_leaves_the_rest_alone(fast, change):
+    assert fast.attend(*fast_attend(**change)) is None
+
+
+def fast_append(**change):
+    f = FakeTensor
+    row = (8 * 64, 64, 1)
+    a = dict(q4=False, q=f((3, 4, 64), torch.float16, stride=row), k=f((3, 2, 64), torch.float16, stride=row),
+             v=f((3, 2, 64), torch.float16, stride=row), pos=f((3,), torch.int32), cs=f((9, 32), torch.float32),
+             slots=f((3,), torch.int64), kp=f((32, 2, 64), torch.float16), vp=f((32, 2, 64), torch.float16), inter=False,
+             q_out=f((3, 4, 64), torch.float16, at=2 * P), flags=0, stream=None)
+    return list((a | change).values())
+
+
+def test_fast_append_makes_the_call(fast):
+    assert fast.append(*fast_append()) == lib.PKV_ERR_CUDA
+    assert fast.append(*fast_append(cs=FakeTensor((9, 24), torch.float32))) == lib.PKV_ERR_UNSUPPORTED
+    assert fast.gather(FakeTensor((4, 2, 640), torch.uint8), FakeTensor((4, 2, 640), torch.uint8),
+                       FakeTensor((1, 2), torch.int32), FakeTensor((1, 32, 2, 64), torch.float16),
+                       FakeTensor((1, 32, 2, 64), torch.float16), 1, None, 0, None) == lib.PKV_ERR_CUDA
+
+
+@pytest.mark.parametrize("change", [
+    dict(q=None), dict(cs=None), dict(q_out=None), dict(k=FakeTensor((3, 2, 64), torch.float16, stride=(512, 1, 2))),
+    dict(q=FakeTensor((2, 4, 64), torch.float16)), dict(v=FakeTensor((3, 2, 64), torch.bfloat16)),
+    dict(pos=FakeTensor((3,), torch.int64)), dict(pos=FakeTensor((4,), torch.int32)), dict(cs=FakeTensor((9, 0), torch.float32)),
+    dict(slots=FakeTensor((3,), torch.int32)), dict(kp=FakeTensor((32, 1, 64), torch.float16)), dict(q4=True),
+    dict(slots=FakeTensor((3,), torch.int64, contiguous=False)), dict(v=FakeTensor((3, 2, 64), torch.float16, device=1)),
+])
+def test_fast_append_leaves_the_rest_alone(fast, change):
+    assert fast.append(*fast_append(**change)) is None
