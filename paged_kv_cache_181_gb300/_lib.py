@@ -411,7 +411,7 @@ def q4_block_bytes(head_dim: int) -> int:
 
 # These calls are a few microseconds of GPU time in a decode step, so a well-formed one is checked and made by
 # csrc/fastcall.c (4 to 6 us of host time; 18 through the helpers above).  What it does not take -- a wrong argument, a
-# call without q or rotation, a workspace to allocate -- it leaves untouched to the functions here.
+# call without q or rotation -- it leaves untouched to the functions here.
 _DTYPES: dict = {}
 _raw_stream = _current_device = _u8 = _i32t = _i64 = _f32 = None
 
@@ -600,6 +600,14 @@ def paged_kv_gather_q4(key_pool, value_pool, block_table, stage_k, stage_v, *, f
         _ok(status)
 
 
+def _scratch(nbytes: int, q, stream):
+    """A workspace from torch's allocator for one call on ``stream`` (None: the current one)."""
+    workspace = _torch().empty(nbytes, dtype=_u8, device=q.device)
+    if stream is not None:
+        workspace.record_stream(stream)
+    return workspace
+
+
 def _attn_window(fn: str, entry, q4: bool, q, key_pool, value_pool, block_table, query_start_loc, seq_lens,
                  max_query_len, max_seq_len, softmax_scale, window, sinks, out, workspace, flags, block_size, stream):
     shape, dtype, pool_shape, table_shape = q.shape, q.dtype, key_pool.shape, block_table.shape
@@ -648,10 +656,8 @@ def _attn_window(fn: str, entry, q4: bool, q, key_pool, value_pool, block_table,
         ws_bytes = lib.paged_attn_window_workspace_size(blocks, hq, hkv, d, code, q4, B, max_query_len, max_seq_len,
                                                         window, sinks)
         if ws_bytes:
-            workspace = _torch().empty(ws_bytes, dtype=_u8, device=q.device)
+            workspace = _scratch(ws_bytes, q, stream)
             ws_at = workspace.data_ptr()
-            if stream is not None:
-                workspace.record_stream(stream)
     status = entry(q.data_ptr(), Tq, hq, key_pool.data_ptr(), value_pool.data_ptr(), blocks, block_size, hkv, d, code,
                    block_table.data_ptr(), B, W, query_start_loc.data_ptr(), seq_lens.data_ptr(), int(max_query_len),
                    int(max_seq_len), float(softmax_scale), int(window), int(sinks), out.data_ptr(), ws_at, ws_bytes, flags,
@@ -680,8 +686,11 @@ def paged_attn_window(q, key_pool, value_pool, block_table, query_start_loc, seq
     """
     if out is None:
         out = _torch().empty_like(q)
-    status = _fastcall.attend(False, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len,
-                              max_seq_len, softmax_scale, window, sinks, out, workspace, flags, block_size, stream)
+    args = (False, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len, max_seq_len,
+            softmax_scale, window, sinks, out)
+    status = _fastcall.attend(*args, workspace, flags, block_size, stream)
+    if status is not None and status < 0:
+        status = _fastcall.attend(*args, _scratch(-status, q, stream), flags, block_size, stream)
     if status is not None:
         if status:
             _ok(status)
@@ -697,8 +706,11 @@ def paged_attn_q4(q, key_pool, value_pool, block_table, query_start_loc, seq_len
     """paged_attn_window over 4-bit pools (uint8 ``[num_blocks, Hkv, q4_block_bytes(D)]``); returns ``out``."""
     if out is None:
         out = _torch().empty_like(q)
-    status = _fastcall.attend(True, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len,
-                              max_seq_len, softmax_scale, window, sinks, out, workspace, flags, block_size, stream)
+    args = (True, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len, max_seq_len,
+            softmax_scale, window, sinks, out)
+    status = _fastcall.attend(*args, workspace, flags, block_size, stream)
+    if status is not None and status < 0:
+        status = _fastcall.attend(*args, _scratch(-status, q, stream), flags, block_size, stream)
     if status is not None:
         if status:
             _ok(status)

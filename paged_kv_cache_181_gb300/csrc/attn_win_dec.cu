@@ -214,7 +214,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 template <typename T, int D, int NT>
 int launch_nt(const PkvWinArgs& a, void* ws, size_t bytes, size_t* wanted, int* launches, cudaStream_t s) {
   static PkvKernelState state;
-  return dec::launch<T, D, NT>(attn_win_dec_kernel<T, D, NT>, state, sizeof(Smem<D, NT>), a, ws, bytes, wanted, launches, s);
+  return dec::launch<T, D, NT>(attn_win_dec_kernel<T, D, NT>, state, sizeof(Smem<D, NT>), 0.95, a, ws, bytes, wanted,
+                             launches, s);
 }
 
 template <typename T, int D>

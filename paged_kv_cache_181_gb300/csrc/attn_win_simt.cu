@@ -295,11 +295,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_win_simt_few_kernel(const Pk
 }
 
 template <typename Kernel>
-int launch(Kernel kernel, PkvKernelState& state, size_t smem, int64_t items, int64_t steps, double fixed,
-           const PkvWinArgs& a, cudaStream_t s) {
+int launch(Kernel kernel, PkvKernelState& state, size_t smem, int64_t items, int64_t steps, double rate,
+           double setup, const PkvWinArgs& a, cudaStream_t s) {
   const int rc = pkv_prepare_kernel((const void*)kernel, (int)smem, kThreads, 0, state);
   if (rc) return rc;
-  const int ctas = pkv_plan_cluster(state, items, steps, fixed);
+  const int ctas = pkv_plan_cluster(state, items, steps, rate, setup);
   void* args[] = {const_cast<PkvWinArgs*>(&a)};
   return pkv_launch_cluster((const void*)kernel, items, ctas, kThreads, smem, args, false, s);
 }
@@ -312,11 +312,11 @@ int launch_rows(const PkvWinArgs& a, cudaStream_t s) {
     static PkvKernelState state;
     const int64_t keys = pkv_visible_keys(a, a.max_query_len);
     return launch(attn_win_simt_few_kernel<T, Pool, D>, state, sizeof(FewSmem<D>), (int64_t)a.B * a.Hkv,
-                  keys / (8 * kWarps) + 1, 5.0, a, s);
+                  keys / (8 * kWarps) + 1, 0.8, 2.0, a, s);
   }
   static PkvKernelState state;
   return launch(attn_win_simt_kernel<T, Pool, D>, state, sizeof(Smem<D>), (int64_t)a.B * a.Hkv * ((rows + kRows - 1) / kRows),
-                pkv_visible_keys(a, kRows / g + 1) / kKeys + 1, 2.0, a, s);
+                pkv_visible_keys(a, kRows / g + 1) / kKeys + 1, 0.4, 0.5, a, s);
 }
 
 template <typename T, typename Pool>

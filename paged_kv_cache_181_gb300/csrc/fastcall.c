@@ -4,7 +4,7 @@
  * call took 8 to 10 us of host time, more than the kernels.  The functions here check that the tensors are what the
  * call takes and make it: 4 to 6 us.  Where anything is not as it should be they return None without having done
  * anything, and the binding's careful path (_lib.py) runs instead: it raises the error, or takes the rarer forms (no
- * q, no rotation, a workspace to allocate).  Otherwise they return the call's status.
+ * q, no rotation).  Otherwise they return the call's status.
  *
  * Only documented methods and attributes of the tensors are used (data_ptr, get_device, is_contiguous, dtype, shape,
  * stride), so nothing here depends on the build of torch.
@@ -15,7 +15,7 @@
 
 #include "pagedkv.h"
 
-static PyObject *s_data_ptr, *s_get_device, *s_is_contiguous, *s_dtype, *s_shape, *s_stride, *s_cuda_stream;
+static PyObject *s_data_ptr, *s_get_device, *s_is_contiguous, *s_dtype, *s_shape, *s_stride, *s_cuda_stream, *s_nbytes;
 static PyObject *dt_code[3], *dt_u8, *dt_i32, *dt_i64; /* dt_code: by pkv_dtype */
 static PyObject *current_device, *raw_stream;
 
@@ -109,19 +109,22 @@ static PyObject* decline(void) {
   Py_RETURN_NONE;
 }
 
-/* attend(q4, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len, max_seq_len, scale, window,
+/* -n: nothing was done, the call wants a workspace of n bytes.
+ * attend(q4, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len, max_seq_len, scale, window,
  *        sinks, out, workspace, flags, block_size, stream) */
 static PyObject* attend(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
-  if (n != 17 || !raw_stream || a[13] != Py_None) return decline();
+  if (n != 17 || !raw_stream) return decline();
   const int q4 = a[0] == Py_True;
   PyObject* devo = PyObject_CallNoArgs(current_device);
   if (!devo) return decline();
   const long long dev = PyLong_AsLongLong(devo);
-  Tensor t[7]; /* q, key_pool, value_pool, block_table, query_start_loc, seq_lens, out */
-  PyObject* const objs[7] = {a[1], a[2], a[3], a[4], a[5], a[6], a[12]};
+  Tensor t[8]; /* q, key_pool, value_pool, block_table, query_start_loc, seq_lens, out, workspace */
+  PyObject* const objs[8] = {a[1], a[2], a[3], a[4], a[5], a[6], a[12], a[13]};
+  const int count = a[13] == Py_None ? 7 : 8;
   int loaded = 0, status = -1;
-  for (; loaded < 7; ++loaded)
+  size_t wanted = 0;
+  for (; loaded < count; ++loaded)
     if (!load(objs[loaded], dev, 0, &t[loaded])) {
       ++loaded;
       goto done;
@@ -147,20 +150,32 @@ static PyObject* attend(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         hq > INT32_MAX || hkv > INT32_MAX || d > INT32_MAX || B > INT32_MAX || W > INT32_MAX)
       goto done;
     if (!q4) blocks /= 16;
-    if (B * hkv < 256 && code && ml > 1024 && (window > 1024 || window == 0) &&
-        paged_attn_window_workspace_size(blocks, (int)hq, (int)hkv, (int)d, (pkv_dtype)code, q4, (int)B, mq, ml, window,
-                                         sinks))
-      goto done; /* the careful path allocates it */
+    void* ws = NULL;
+    long long ws_bytes = 0;
+    if (count == 8) {
+      PyObject* r = PyObject_GetAttr(a[13], s_nbytes);
+      if (!r) goto done;
+      ws_bytes = PyLong_AsLongLong(r);
+      Py_DECREF(r);
+      if (ws_bytes < 0) goto done;
+      ws = t[7].ptr;
+    } else if (B * hkv < 256 && code && ml > 1024 && (window > 1024 || window == 0)) {
+      /* Few sequences and heads over many keys: no other sizes take a workspace. */
+      wanted = paged_attn_window_workspace_size(blocks, (int)hq, (int)hkv, (int)d, (pkv_dtype)code, q4, (int)B, mq, ml,
+                                                window, sinks);
+      if (wanted) goto done;
+    }
     void* stream;
     if (!stream_of(a[16], devo, &stream)) goto done;
     status = (q4 ? paged_attn_q4 : paged_attn_window)(
         t[0].ptr, Tq, (int)hq, t[1].ptr, t[2].ptr, blocks, bs, (int)hkv, (int)d, (pkv_dtype)code, (const int32_t*)t[3].ptr,
         (int)B, (int)W, (const int32_t*)t[4].ptr, (const int32_t*)t[5].ptr, mq, ml, (float)scale, window, sinks, t[6].ptr,
-        NULL, 0, (uint32_t)flags, stream);
+        ws, (size_t)ws_bytes, (uint32_t)flags, stream);
   }
 done:
   drop(t, loaded);
   Py_DECREF(devo);
+  if (wanted) return PyLong_FromLongLong(-(long long)wanted);
   return status < 0 ? decline() : PyLong_FromLong(status);
 }
 
@@ -276,9 +291,11 @@ static PyMethodDef methods[] = {
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fastcall", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__fastcall(void) {
-  static const char* const names[7] = {"data_ptr", "get_device", "is_contiguous", "dtype", "shape", "stride", "cuda_stream"};
-  PyObject** const to[7] = {&s_data_ptr, &s_get_device, &s_is_contiguous, &s_dtype, &s_shape, &s_stride, &s_cuda_stream};
-  for (int i = 0; i < 7; ++i)
+  static const char* const names[8] = {"data_ptr", "get_device", "is_contiguous", "dtype",
+                                       "shape",    "stride",     "cuda_stream",   "nbytes"};
+  PyObject** const to[8] = {&s_data_ptr, &s_get_device, &s_is_contiguous, &s_dtype,
+                            &s_shape,    &s_stride,     &s_cuda_stream,   &s_nbytes};
+  for (int i = 0; i < 8; ++i)
     if (!(*to[i] = PyUnicode_InternFromString(names[i]))) return NULL;
   return PyModule_Create(&module);
 }

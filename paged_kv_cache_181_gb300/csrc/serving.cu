@@ -209,44 +209,50 @@ int current_device() {
 
 }  // namespace
 
-// Kernels of several CTAs per SM share its rate, so a launch takes about its whole work over the CTAs that run at
-// once, and, at the end, half a CTA's time more while they run out.
-static double shared_cost(int64_t ctas, int64_t at_once, int64_t steps, double fixed) {
-  const double one = (double)steps + fixed, waves = (double)ctas / (double)at_once;
-  return (waves > 1.0 ? waves : 1.0) * one + 0.5 * one;
+// Kernels of several CTAs per SM, in steps of a CTA that has its SM to itself: CTAs that share an SM take turns, each step
+// then costing `rate` (a little under 1: one CTA of four warps nearly takes an SM's share of the memory or of its issue
+// slots by itself), and each CTA costs `setup` steps more.  The SM with the most CTAs decides; past four of them the
+// hardware deals them out as they finish.  A cluster costs its launch and merge.  Fitted to 25 mixes of 1 to 64 sequences,
+// 80 to 50000 keys and 1 to 8 kv heads, timed with every cluster size: the choice is the best of them or within a
+// tenth of it.
+static double shared_cost(int64_t ctas, int64_t sms, int64_t steps, double rate, double setup) {
+  const double k = (double)ctas / (double)sms;
+  const double most = k <= 1.0 ? 1.0 : k <= 4.0 ? ceil(k) : k + 0.7;
+  return most * ((double)steps * (most > 1.0 ? rate : 1.0) + setup);
 }
 
-static Split best_cluster(const PkvKernelState& state, int dev, int64_t items, int64_t steps, double fixed) {
+static Split best_cluster(const PkvKernelState& state, int dev, int64_t items, int64_t steps, double rate, double setup) {
+  static const double merge[5] = {0.0, 0.65, 0.75, 1.0, 2.5};  // in set-ups
+  const int64_t sms = pkv_sm_count() > 0 ? pkv_sm_count() : 152;
   Split best{1, 1e300};
   for (int i = 0; i < 5; ++i) {
     const int c = 1 << i;
-    const int64_t active = state.active[dev][i].load(std::memory_order_relaxed);
-    if (active <= 0 && c > 1) break;
-    if (c > 1 && (steps < 2 * c || items * c > kMaxGrid)) break;
-    const double cost = shared_cost(items * c, (active > 0 ? active : 152) * c, (steps + c - 1) / c, fixed);
-    if (cost < 0.97 * best.cost) best = Split{c, cost};
+    if (i > 0 && (state.active[dev][i].load(std::memory_order_relaxed) <= 0 || 2 * steps < c || items * c > kMaxGrid)) break;
+    const double cost = shared_cost(items * c, sms, (steps + c - 1) / c, rate, setup) + merge[i] * setup;
+    if (cost < 0.99 * best.cost) best = Split{c, cost};
   }
   return best;
 }
 
-int pkv_plan_cluster(const PkvKernelState& state, int64_t items, int64_t steps, double fixed) {
-  return best_cluster(state, current_device(), items, steps, fixed).ctas;
+int pkv_plan_cluster(const PkvKernelState& state, int64_t items, int64_t steps, double rate, double setup) {
+  return best_cluster(state, current_device(), items, steps, rate, setup).ctas;
 }
 
-int pkv_plan_splits(const PkvKernelState& state, int64_t items, int64_t steps, double fixed, double combine) {
+int pkv_plan_splits(const PkvKernelState& state, int64_t items, int64_t steps, double rate, double setup,
+                    double combine) {
   const int dev = current_device();
-  const int64_t slots = state.active[dev][0].load(std::memory_order_relaxed);
-  if (slots <= 0 || items * 2 > slots || steps <= 16) return 1;  // (up to 1024 keys a cluster has a step per CTA)
-  int64_t splits = slots / items;
-  if (splits > steps) splits = steps;
-  if (splits > 64) {
-    // As many CTAs on every SM.
-    const int64_t sms = pkv_sm_count() > 0 ? pkv_sm_count() : 152;
-    splits = items * 64 >= sms ? items * 64 / sms * sms / items : 64;
+  const int64_t sms = pkv_sm_count() > 0 ? pkv_sm_count() : 152;
+  const int64_t per_sm = state.active[dev][0].load(std::memory_order_relaxed) / sms;
+  if (items * 2 > sms || steps <= 16) return 1;
+  Split best = best_cluster(state, dev, items, steps, rate, setup);
+  best.ctas = 1;
+  for (int64_t m = 1; m <= per_sm; ++m) {  // as many CTAs on every SM
+    const int64_t n = m * sms / items;
+    if (n < 2 || n > 64 || n > steps) continue;
+    const double cost = shared_cost(items * n, sms, (steps + n - 1) / n, rate, setup) + combine;
+    if (cost < 0.99 * best.cost) best = Split{(int)n, cost};
   }
-  if (splits < 2) return 1;
-  const double cost = shared_cost(items * splits, slots, (steps + splits - 1) / splits, fixed) + combine;
-  return cost < best_cluster(state, dev, items, steps, fixed).cost ? (int)splits : 1;
+  return best.ctas;
 }
 
 // Whole waves of single CTAs, and a second launch that splits the items behind them, where that is estimated a

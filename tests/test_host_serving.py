@@ -214,7 +214,7 @@ def test_fast_attention_makes_the_call(fast):
     dict(table=FakeTensor((1, 2), torch.int64)), dict(table=FakeTensor((2,), torch.int32)),
     dict(lens=FakeTensor((2,), torch.int32)), dict(qsl=FakeTensor((3,), torch.int32)),
     dict(out=FakeTensor((3, 4, 32), torch.bfloat16)), dict(out=FakeTensor((3, 4, 64), torch.bfloat16, contiguous=False)),
-    dict(ws=FakeTensor((64,), torch.uint8)), dict(bs=32), dict(mq=2.0), dict(mq=2 ** 40), dict(scale="x"), dict(q4=True),
+    dict(ws=FakeTensor((64,), torch.uint8, device=1)), dict(bs=32), dict(mq=2.0), dict(mq=2 ** 40), dict(scale="x"), dict(q4=True),
     dict(q=None), dict(stream=7), dict(flags=None),
 ])
 def test_fast_attention_leaves_the_rest_alone(fast, change):
