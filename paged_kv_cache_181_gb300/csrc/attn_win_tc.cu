@@ -15,12 +15,21 @@
 // Warps: 1 issues the MMAs and owns TMEM; 4-7 and 8-11 are the softmax of the two tiles, one row per thread; and
 //   16-bit pools: 0 loads Q and the key tiles by TMA (one box per page), 3 the value tiles;
 //   4-bit pools:  0 copies whole records to shared memory, 2, 3 and 12-15 turn their codes into the fp16 numbers they
-//                 stand for and store them swizzled as TMA would; Q is converted to fp16 by the softmax threads, each row scaled by a power of two.
-//                 Channels of a code word come out as (0,4), (1,5), (2,6), (3,7): Q's and the output's channels are
-//                 permuted to match, which is free, instead of the codes.
+//                 stand for and store them swizzled as TMA would; Q is converted to fp16 by the softmax threads, each
+//                 row scaled by a power of two.  Channels of a code word come out as (0,4), (1,5), (2,6), (3,7): Q's
+//                 and the output's channels are permuted to match, which is free, instead of the codes.
+// CTAs are persistent: warp 0 asks the hardware for a CTA that has not started yet, cancels its launch and takes its
+// item (clusterlaunchcontrol), and the roles go on to it each at its own pace: the producers load the next item's
+// keys and queries while the softmax warps finish the last one.  4096 tokens x 40 heads over 8 kv heads, D = 128, with a
+// window of 64: 46 us instead of 69 with a CTA an item; window 1024: 145 instead of 163.  (Clusters keep to their item.)
+//
+// What bounds it: a tile's chain.  Its probabilities overwrite its scores in TMEM, so each 128 keys take the softmax
+// (1700 cycles of a row's 128 exponentials; masked ones 2800 and more), its products (1024 cycles for both tiles) and
+// the hand-overs one after the other, about 3500 cycles, and only the other tile's work fills the gaps.  The tensor
+// cores reach 1.19 PFLOP/s over 4000-key windows, 1.07 with 4-bit pools, where turning codes into numbers adds to it.
 // The order of MMAs, the ring of slots shared by key and value tiles, the lazy rescale and the register split between
 // warpgroups are those of the prefix-mask kernel (attn_tc.cu), which says why.
-// Every mbarrier wait is bounded in time (1 s); on expiry the CTA records PKV_DEVERR_TIMEOUT and unwinds.
+// Every mbarrier wait is bounded in time (1 s, or 60 for the next item); on expiry the CTA records PKV_DEVERR_TIMEOUT and unwinds.
 
 #include <cuda.h>
 
@@ -45,14 +54,16 @@ template <bool POOLQ4>
 struct Roles {
   static constexpr int kThreads = POOLQ4 ? 512 : 384;
   static constexpr int kRegs = POOLQ4 ? kLaunchRegsQ4 : kLaunchRegs;
-  static constexpr int kLow = POOLQ4 ? 72 : 104, kHigh = POOLQ4 ? 184 : 200;
+  static constexpr int kLow = POOLQ4 ? 72 : 136, kHigh = POOLQ4 ? 184 : 184;
   static_assert((kThreads - 256) * kLow + 256 * kHigh == kThreads * kRegs, "register split must add up");
 };
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
+constexpr uint64_t kItemLimitNs = 60 * kWaitLimitNs;  // of a role without work in an item: 2^31 keys take 30 s
 constexpr float kRescale = 8.f;  // log2 units
 constexpr int kDequantWarps = 6;
-constexpr double kFixedTiles = 4.0;  // a CTA's set-up and epilogue, in key tiles of its time
+constexpr int kAskAhead = 4;  // key tiles an item has left to load when its CTA asks for the next one
+constexpr double kFixedTiles = 4.0;  // a CTA's set-up and epilogue, in key tiles of its time (1 to 4 plan alike)
 
 template <int D, bool POOLQ4>
 struct Cfg {
@@ -64,6 +75,16 @@ struct Cfg {
   static constexpr int OSTRIDE = D + 4;       // floats between rows staged for the merge
 };
 
+// An item as its CTA works on it.
+struct Item {
+  int n;        // key tiles of this CTA; -1: no more items
+  int t_begin;  // the first of them
+  int q0, Sq, kvh, b;
+  int i0, n_q;  // first local query token; tiles with rows
+  int base;     // position of local query 0
+  WinPages pg;
+};
+
 template <int D, bool POOLQ4>
 struct alignas(1024) WinSmem {
   using C = Cfg<D, POOLQ4>;
@@ -72,7 +93,10 @@ struct alignas(1024) WinSmem {
   uint8_t raw[POOLQ4 ? C::NRAW : 1][POOLQ4 ? C::RAW : 16];  // records of 4-bit tiles
   uint64_t full[C::NSLOT], empty[C::NSLOT];
   uint64_t raw_full[3], raw_empty[3];
-  uint64_t q_full, s_full[2], p_full[2], mma_done;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t info_full[2], info_empty[2], clc_full;
+  alignas(16) uint4 clc;  // the scheduler's last answer
+  Item info[2];           // the item in work, and the one to come
   uint32_t tmem_base;
   int abort, skip;
   // The merge stages 2 BM rows of OSTRIDE floats from kv on.
@@ -119,20 +143,26 @@ PKV_DEVINLINE void note_abort(Smem& sm, unsigned int* err) {
   pkv_raise(err, PKV_DEVERR_TIMEOUT);
 }
 
-PKV_DEVINLINE bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int lane) {
+PKV_DEVINLINE bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int lane,
+                             uint64_t limit = kWaitLimitNs) {
   bool ok = true;
-  if (lane == 0) ok = ptx::mbar_wait(bar, parity, abort, kWaitLimitNs);
+  if (lane == 0) ok = ptx::mbar_wait(bar, parity, abort, limit);
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
-// One warp loads a 16-bit key or value tile: pages [8 kt, 8 kt + 8) of the item's list, a lane per page.
+// Lane k < 8: block of page k of key tile kt.
+PKV_DEVINLINE int tile_block(const PkvWinArgs& a, const WinPages& pg, int b, int kt, int lane) {
+  const int v = kPages * kt + lane;
+  return lane < kPages && v < pg.n ? win_block(a, b, pg.page(v)) : 0;
+}
+
+// One warp loads a 16-bit key or value tile: pages [8 kt, 8 kt + 8) of the item's list, a lane per page (block `blk`).
 template <int D>
 PKV_DEVINLINE void load_tile(uint8_t* dst, const WinMaps& maps, bool is_v, uint64_t* full, const PkvWinArgs& a,
-                             const WinPages& pg, int b, int kvh, int kt, int lane) {
+                             const WinPages& pg, int blk, int kvh, int kt, int lane) {
   const int v = kPages * kt + lane;
   const bool there = lane < kPages && v < pg.n;
   const int page = there ? pg.page(v) : 0;
-  const int blk = there ? win_block(a, b, page) : 0;
   unsigned seen = there ? 0xffffu : 0u;  // rows of the page that some query sees
   if (is_v) {
     if (there) {
@@ -169,12 +199,68 @@ PKV_DEVINLINE void load_tile(uint8_t* dst, const WinMaps& maps, bool is_v, uint6
   }
 }
 
+// Ask for the launch of a CTA that has not started to be cancelled: 16 bytes of answer at `dst`, counted on `bar`.
+PKV_DEVINLINE void clc_try_cancel(void* dst, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          ptx::smem_u32(dst)),
+      "r"(ptx::smem_u32(bar))
+      : "memory");
+}
+// Whether the answer holds a cancelled CTA, and its blockIdx.x.
+PKV_DEVINLINE bool clc_answer(const void* src, uint32_t* cta) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n"
+      ".reg .b128 r;\n"
+      ".reg .pred p;\n"
+      "ld.shared.b128 r, [%2];\n"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "mov.u32 %1, 0;\n"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n"
+      "}\n"
+      : "=r"(ok), "=r"(x)
+      : "r"(ptx::smem_u32(src))
+      : "memory");
+  *cta = x;
+  return ok != 0;
+}
+
+// Item u of the grid for this CTA (its cluster's rank); false: no queries there.
+// Items with the latest queries (the most keys) come first; the kv heads of one stretch of queries run together.
+PKV_DEVINLINE bool decode_item(const PkvWinArgs& a, uint32_t u, Item& it) {
+  const int g = a.Hq / a.Hkv, TM = BM / g;  // tokens per tile
+  const int n_qp = (a.max_query_len + 2 * TM - 1) / (2 * TM);
+  it.kvh = u % a.Hkv;
+  u /= a.Hkv;
+  it.b = u % a.B;
+  const int qp = n_qp - 1 - (int)(u / a.B);
+  const uint32_t rank = cluster_rank(), n_cta = cluster_size();
+  const WinRow row = win_row(a, it.b, qp == 0 && it.kvh == 0 && rank == 0);
+  it.q0 = row.q0;
+  it.Sq = row.Sq;
+  it.i0 = qp * 2 * TM;
+  if (it.i0 >= row.Sq) return false;
+  it.n_q = it.i0 + TM < row.Sq ? 2 : 1;
+  it.base = row.L - row.Sq;
+  const int last = row.Sq < it.i0 + 2 * TM ? row.Sq : it.i0 + 2 * TM;  // one past the item's last token
+  it.pg = win_pages(it.base + it.i0, it.base + last - 1, a.window, a.sinks);
+  const int n_tiles = (it.pg.n + kPages - 1) / kPages;
+  const int per = (n_tiles + (int)n_cta - 1) / (int)n_cta;
+  it.t_begin = (int)rank * per;
+  const int t_end = n_tiles < it.t_begin + per ? n_tiles : it.t_begin + per;
+  it.n = t_end > it.t_begin ? t_end - it.t_begin : 0;
+  return true;
+}
+
 template <int D, typename T, bool OPBF16, bool POOLQ4>
 __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
     attn_win_tc_kernel(const __grid_constant__ WinMaps maps, const PkvWinArgs a, const uint32_t first_item) {
   using C = Cfg<D, POOLQ4>;
   constexpr int kThreads = Roles<POOLQ4>::kThreads;
   constexpr bool OUTBF16 = !std::is_same<T, __half>::value;
+  constexpr int kReaders = POOLQ4 ? 16 : 11;  // warps that read an item (with 16-bit pools warp 2 has no work)
   extern __shared__ uint8_t smem_raw[];
   using Smem = WinSmem<D, POOLQ4>;
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -182,37 +268,9 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
   const int g = a.Hq / a.Hkv;
   const int TM = BM / g;  // tokens per tile
   const uint32_t rank = cluster_rank(), n_cta = cluster_size();
-  // Items with the latest queries (the most keys) first; the kv heads of one stretch of queries run together.
-  uint32_t item = first_item + blockIdx.x / n_cta;
   // A second launch, for the items behind whole waves, may start as soon as this one's last CTAs run.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int n_qp = (a.max_query_len + 2 * TM - 1) / (2 * TM);
-  const int kvh = item % a.Hkv;
-  item /= a.Hkv;
-  const int b = item % a.B, qp = n_qp - 1 - item / a.B;
-  const WinRow row = win_row(a, b, tid == 0 && qp == 0 && kvh == 0 && rank == 0);
-  const int i0 = qp * 2 * TM;
-  if (i0 >= row.Sq) {  // the whole cluster leaves
-    if (first_item) asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
-  const int n_q = i0 + TM < row.Sq ? 2 : 1;
-  const int base = row.L - row.Sq;
-  const int last = row.Sq < i0 + 2 * TM ? row.Sq : i0 + 2 * TM;  // one past the CTA's last token
-  const WinPages pg = win_pages(base + i0, base + last - 1, a.window, a.sinks);
-  const int n_tiles = (pg.n + kPages - 1) / kPages;
-  const int per = (n_tiles + (int)n_cta - 1) / (int)n_cta;
-  const int t_begin = (int)rank * per;
-  const int t_end = n_tiles < t_begin + per ? n_tiles : t_begin + per;
-  int n = t_end > t_begin ? t_end - t_begin : 0;
-
-  const int grp = warp >= 8 ? 1 : 0;
   const bool is_softmax = warp >= 4 && warp < 12;
-  const int quarter = warp & 3;
-  const int trow = quarter * 32 + lane;             // row of the tile
-  const int tok = i0 + grp * TM + trow / g;         // local query token of the row
-  const bool valid = is_softmax && trow < TM * g && tok < row.Sq;
-  float sl2 = a.scale * 1.4426950408889634f;
 
   if (tid == 0) {
     for (int s = 0; s < C::NSLOT; ++s) {
@@ -223,27 +281,27 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
       ptx::mbar_init(&sm.raw_full[s], 1);
       ptx::mbar_init(&sm.raw_empty[s], kDequantWarps);
     }
-    ptx::mbar_init(&sm.q_full, 1);
     for (int w = 0; w < 2; ++w) {
+      ptx::mbar_init(&sm.q_full[w], POOLQ4 ? 128 : 1);
       ptx::mbar_init(&sm.s_full[w], 1);
       ptx::mbar_init(&sm.p_full[w], 128);
+      ptx::mbar_init(&sm.q_empty[w], 1);
+      ptx::mbar_init(&sm.o_full[w], 1);
+      ptx::mbar_init(&sm.info_full[w], 1);
+      ptx::mbar_init(&sm.info_empty[w], kReaders);
     }
-    ptx::mbar_init(&sm.mma_done, 1);
+    ptx::mbar_init(&sm.clc_full, 1);
     sm.abort = 0;
     // After a pipeline timeout in an earlier launch results are invalid: do not wait for it again.
     sm.skip = (*(volatile unsigned int*)a.err & PKV_DEVERR_TIMEOUT) != 0;
     ptx::fence_mbar_init();
-    if (POOLQ4) {
-      ptx::mbar_arrive(&sm.q_full);  // Q is in place after the barrier below
-    } else {
-      ptx::mbar_arrive_expect_tx(&sm.q_full, (uint32_t)(n_q * TM * g * D * 2));
-      for (int t = 0; t < n_q; ++t)
-#pragma unroll
-        for (int dh = 0; dh < D / 64; ++dh)  // tokens past the last one read as zeros
-          tma_load_4d(sm.q[t] + dh * (BM * 128), &maps.q, dh * 64, 0, kvh, row.q0 + i0 + t * TM, &sm.q_full);
-    }
   }
+  Item mine;
+  mine.n = -1;
+  bool there = false;
+  if (warp == 0 && lane == 0) there = decode_item(a, first_item + blockIdx.x / n_cta, mine);
   if (!POOLQ4 && warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&maps.q);
     ptx::prefetch_tmap(&maps.kb);
     ptx::prefetch_tmap(&maps.vb);
   }
@@ -251,91 +309,200 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
     ptx::tmem_alloc(&sm.tmem_base, kTmemCols);
     ptx::tmem_relinquish();
   }
-  if (POOLQ4 && is_softmax && grp < n_q) {
-    // The row's Q in fp16, scaled so that its largest magnitude lies in [2^13, 2^14).
-    const int64_t at = (((int64_t)row.q0 + tok) * a.Hq + kvh * g + trow % g) * D;
-    const uint4* src = reinterpret_cast<const uint4*>((const T*)a.q + at);
-    float top = 0.f;
-    if (valid)
-#pragma unroll 4
-      for (int v = 0; v < D / 8; ++v) {
-        const uint4 x = __ldg(src + v);
-        const T* e = reinterpret_cast<const T*>(&x);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(pkv_to_f32<T>(e[c])));
-      }
-    const int e2 = top > 0.f && top <= 3.402823466e38f ? min(13 - ilogbf(top), 64) : 0;
-    sl2 = scalbnf(sl2, -e2);
-#pragma unroll 4
-    for (int v = 0; v < D / 8; ++v) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (valid) x = __ldg(src + v);
-      const T* e = reinterpret_cast<const T*>(&x);
-      uint32_t w[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        w[c] = ptx::pack_f16x2(scalbnf(pkv_to_f32<T>(e[c]), e2), scalbnf(pkv_to_f32<T>(e[c + 4]), e2));
-      *reinterpret_cast<uint4*>(sm.q[grp] + (v >> 3) * (BM * 128) + trow * 128 + (((v & 7) ^ (trow & 7)) << 4)) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    ptx::fence_proxy_async_smem();
-  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
 
   const uint32_t tmem = sm.tmem_base;
-  if (sm.skip) n = 0;
+  const bool skip = sm.skip != 0;
   constexpr uint32_t O_COL[2] = {256, 256 + D};
   constexpr uint32_t IDESC_QK = ptx::idesc_f16(BM, BN, OPBF16 ? 1 : 0, 0);
   constexpr uint32_t IDESC_PV = ptx::idesc_f16(BM, D, OPBF16 ? 1 : 0, 1);
 
+  // Every role walks the items: wait for the next one, work, hand its place back.  All lanes call both.
+  int seq = 0;
+  auto next_item = [&]() -> bool {
+    const bool ok = warp_wait(&sm.info_full[seq & 1], (seq >> 1) & 1, &sm.abort, lane, kItemLimitNs);
+    if (!ok) {
+      if (lane == 0) note_abort(sm, a.err);
+      return false;
+    }
+    __syncwarp();
+    return sm.info[seq & 1].n >= 0;
+  };
+  auto done_item = [&]() {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&sm.info_empty[seq & 1]);
+    ++seq;
+  };
+  int tb = 0;  // key tiles of the items before this one: the ring goes on over them
+
   if (!is_softmax) {
     ptx::regs_dec<Roles<POOLQ4>::kLow>();
-    if (!POOLQ4 && (warp == 0 || warp == 3)) {
-      // ------------------------------------------------------------ producers: warp 0 key tiles, warp 3 value tiles
-      if (warp == 0 && n == 0 && lane == 0) {
-        int never = 0;  // nothing will wait for Q, but its copy must land before the CTA exits
-        ptx::mbar_wait(&sm.q_full, 0, &never, kWaitLimitNs);
+    // Scheduling, by one lane: publish the item in hand, then find the next one.  It is asked for when kAskAhead tiles
+    // of this item are left to load: an item that is claimed earlier may wait here while another SM falls idle
+    // (2048 queries over 16384 keys, 128 tiles an item: asked for at the start 674 us, so 556).
+    bool have = true, pending = false;
+    uint32_t answers = 0;
+    int published = 0;
+    auto ask = [&]() {
+      if (!have || pending || n_cta > 1) return;
+      ptx::mbar_arrive_expect_tx(&sm.clc_full, 16);
+      clc_try_cancel(&sm.clc, &sm.clc_full);
+      pending = true;
+    };
+    auto publish = [&]() -> bool {  // the item in hand, or that there is none
+      if (!have || there) {
+        const int slot = published & 1;
+        if (published >= 2 && !ptx::mbar_wait(&sm.info_empty[slot], ((published >> 1) - 1) & 1, &sm.abort, kItemLimitNs))
+          return false;
+        if (!have)
+          mine.n = -1;
+        else if (skip)
+          mine.n = 0;
+        sm.info[slot] = mine;
+        ptx::mbar_arrive(&sm.info_full[slot]);
+        ++published;
       }
-      for (int idx = warp == 0 ? 0 : 1; idx < 2 * n; idx += 2) {
-        if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) break;
-        const int pos = idx % C::NSLOT, use = idx / C::NSLOT;
-        if (idx >= C::NSLOT && !warp_wait(&sm.empty[pos], (use - 1) & 1, &sm.abort, lane)) {
-          if (lane == 0) note_abort(sm, a.err);
-          break;
+      return true;
+    };
+    auto advance = [&]() -> bool {  // the next item in hand
+      if (n_cta > 1) {
+        have = false;
+        return true;
+      }
+      ask();
+      if (!ptx::mbar_wait(&sm.clc_full, answers & 1, &sm.abort, kWaitLimitNs)) return false;
+      ++answers;
+      pending = false;
+      uint32_t cta = 0;
+      have = clc_answer(&sm.clc, &cta);
+      ptx::fence_proxy_async_smem();  // read before the next answer is written
+      if (have) there = decode_item(a, first_item + cta, mine);
+      return true;
+    };
+    auto finish = [&]() {  // an answer under way must land before the shared memory goes away
+      int never = 0;
+      if (pending) ptx::mbar_wait(&sm.clc_full, answers & 1, &never, kWaitLimitNs);
+    };
+    // Until an item is published (the first, and each one that the last step found).
+    auto schedule = [&](bool first) -> bool {
+      bool ok = true;
+      if (lane == 0) {
+        if (!first) ok = advance();
+        while (ok) {
+          const int before = published;
+          ok = publish();
+          if (!ok || published > before) break;  // (an item without queries is passed over)
+          ok = advance();
         }
-        load_tile<D>(sm.kv[pos], maps, idx & 1, &sm.full[pos], a, pg, b, kvh, t_begin + (idx >> 1), lane);
+        if (!ok) note_abort(sm, a.err);
       }
+      return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    };
+    if (!POOLQ4 && (warp == 0 || warp == 3)) {
+      // ------------------------------------------------------------ producers: warp 0 Q and key tiles, warp 3 value tiles
+      int loaded[2] = {0, 0};  // Q tiles
+      bool go = warp == 3 || schedule(true);
+      while (go && next_item()) {
+        const Item& it = sm.info[seq & 1];
+        const int n = it.n;
+        const WinPages pg = it.pg;
+        int blk = n > 0 ? tile_block(a, pg, it.b, it.t_begin, lane) : 0;  // fetched a tile ahead
+        bool ok = true;
+        if (warp == 0 && n > 0) {
+          for (int t = 0; t < it.n_q && ok; ++t) {
+            // The score MMAs of the tile's last item must be done with its place.
+            if (loaded[t] > 0 && !warp_wait(&sm.q_empty[t], (loaded[t] - 1) & 1, &sm.abort, lane)) {
+              if (lane == 0) note_abort(sm, a.err);
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              ptx::mbar_arrive_expect_tx(&sm.q_full[t], (uint32_t)(TM * g * D * 2));
+#pragma unroll
+              for (int dh = 0; dh < D / 64; ++dh)  // tokens past the last one read as zeros
+                tma_load_4d(sm.q[t] + dh * (BM * 128), &maps.q, dh * 64, 0, it.kvh, it.q0 + it.i0 + t * TM, &sm.q_full[t]);
+            }
+            ++loaded[t];
+          }
+          if (!ok) break;
+        }
+        for (int j = 0; j < n; ++j) {
+          if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) {
+            ok = false;
+            break;
+          }
+          if (warp == 0 && lane == 0 && j + kAskAhead >= n) ask();
+          const int idx = 2 * (tb + j) + (warp == 3 ? 1 : 0);
+          const int pos = idx % C::NSLOT, use = idx / C::NSLOT;
+          if (use > 0 && !warp_wait(&sm.empty[pos], (use - 1) & 1, &sm.abort, lane)) {
+            if (lane == 0) note_abort(sm, a.err);
+            ok = false;
+            break;
+          }
+          const int ahead = j + 1 < n ? tile_block(a, pg, it.b, it.t_begin + j + 1, lane) : 0;
+          load_tile<D>(sm.kv[pos], maps, warp == 3, &sm.full[pos], a, pg, blk, it.kvh, it.t_begin + j, lane);
+          blk = ahead;
+        }
+        if (!ok) break;
+        tb += n;
+        done_item();
+        if (warp == 0) go = schedule(false);
+      }
+      if (warp == 0 && lane == 0) finish();
       if (warp == 0 && *(volatile int*)&sm.abort && lane == 0) {
-        int dummy = 0;  // let copies already issued land before the shared memory goes away
-        ptx::mbar_wait(&sm.q_full, 0, &dummy, kWaitLimitNs);
+        int never = 0;  // let copies already issued land before the shared memory goes away
+        for (int t = 0; t < 2; ++t)
+          if (loaded[t]) ptx::mbar_wait(&sm.q_full[t], (loaded[t] - 1) & 1, &never, kWaitLimitNs);
       }
     } else if (POOLQ4 && warp == 0) {
       // ------------------------------------------------------------ 4-bit tiles: a lane per page copies its record
-      int ids = 0;
-      for (int idx = 0; idx < 2 * n; ++idx) {
-        if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) break;
-        const int v = kPages * (t_begin + (idx >> 1)) + lane;
-        const bool there = lane < kPages && v < pg.n;
-        if (!(idx & 1) && there) ids = win_block(a, b, pg.page(v));
-        const int pos = idx % 3, use = idx / 3;
-        if (use > 0 && !warp_wait(&sm.raw_empty[pos], (use - 1) & 1, &sm.abort, lane)) {
-          if (lane == 0) note_abort(sm, a.err);
-          break;
+      bool go = schedule(true);
+      while (go && next_item()) {
+        const Item& it = sm.info[seq & 1];
+        const int n = it.n;
+        const WinPages pg = it.pg;
+        bool ok = true;
+        int ids = n > 0 ? tile_block(a, pg, it.b, it.t_begin, lane) : 0, ids_next = 0;  // fetched a tile ahead
+        for (int i = 0; i < 2 * n; ++i) {
+          if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0 && i + 2 * kAskAhead >= 2 * n) ask();
+          const int idx = 2 * tb + i;
+          const int v = kPages * (it.t_begin + (i >> 1)) + lane;
+          const bool page = lane < kPages && v < pg.n;
+          if (i & 1)
+            ids_next = (i >> 1) + 1 < n ? tile_block(a, pg, it.b, it.t_begin + (i >> 1) + 1, lane) : 0;
+          else if (i > 0)
+            ids = ids_next;
+          const int pos = idx % 3, use = idx / 3;
+          if (use > 0 && !warp_wait(&sm.raw_empty[pos], (use - 1) & 1, &sm.abort, lane)) {
+            if (lane == 0) note_abort(sm, a.err);
+            ok = false;
+            break;
+          }
+          const int pages = __popc(__ballot_sync(0xffffffffu, page));
+          if (lane == 0) ptx::mbar_arrive_expect_tx(&sm.raw_full[pos], (uint32_t)(pages * Q4<D>::kRecord));
+          __syncwarp();
+          if (page)
+            bulk_load(sm.raw[POOLQ4 ? pos : 0] + lane * Q4<D>::kRecord,
+                      (const uint8_t*)((i & 1) ? a.v_pool : a.k_pool) + ((int64_t)ids * a.Hkv + it.kvh) * Q4<D>::kRecord,
+                      Q4<D>::kRecord, &sm.raw_full[pos]);
         }
-        const int pages = __popc(__ballot_sync(0xffffffffu, there));
-        if (lane == 0) ptx::mbar_arrive_expect_tx(&sm.raw_full[pos], (uint32_t)(pages * Q4<D>::kRecord));
-        __syncwarp();
-        if (there)
-          bulk_load(sm.raw[POOLQ4 ? pos : 0] + lane * Q4<D>::kRecord,
-                    (const uint8_t*)((idx & 1) ? a.v_pool : a.k_pool) + ((int64_t)ids * a.Hkv + kvh) * Q4<D>::kRecord,
-                    Q4<D>::kRecord, &sm.raw_full[pos]);
+        if (!ok) break;
+        tb += n;
+        done_item();
+        go = schedule(false);
       }
+      if (lane == 0) finish();
       if (*(volatile int*)&sm.abort && lane == 0) {
         // Let copies already issued land before the shared memory goes away.
         int never = 0;
         for (int s = 0; s < 3; ++s) ptx::mbar_wait(&sm.raw_full[s], 0, &never, 1000000ull);
+        for (int s = 0; s < 3; ++s) ptx::mbar_wait(&sm.raw_full[s], 1, &never, 1000000ull);
       }
     } else if (POOLQ4 && warp != 1) {
       // ------------------------------------------------------------ 4-bit tiles: codes to fp16, swizzled as TMA would
@@ -349,321 +516,470 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
       const int pw = warp < 4 ? warp - 2 : warp - 10;
       const int gi = lane % G, rk = lane / G;
       const int x = D == 128 ? (gi >> 1) | ((rk & 1) << 1) : 0;  // chunk order: 0^x, 1^x, 2^x, 3^x
-      for (int idx = 0; idx < 2 * n; ++idx) {
-        if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) break;
-        const int pos = idx % C::NSLOT, use = idx / C::NSLOT, rpos = idx % 3;
-        if (!warp_wait(&sm.raw_full[rpos], (idx / 3) & 1, &sm.abort, lane)) {
-          if (lane == 0) note_abort(sm, a.err);
-          break;
-        }
-        // All of the warp's codes first: the reads overlap each other and the wait for the slot.
-        const uint8_t* raw = sm.raw[POOLQ4 ? rpos : 0];
-        const int p0 = (pw + idx) % kDequantWarps;
-        uint4 code[MINE];
-        uint32_t pair[MINE];
-#pragma unroll
-        for (int k = 0; k < MINE; ++k) {
-          const int r = (p0 + k * kDequantWarps) * KEYS + rk;  // key of the tile
-          const int v = kPages * (t_begin + (idx >> 1)) + (r >> 4);
-          code[k] = make_uint4(0, 0, 0, 0);
-          pair[k] = 0;  // keys that no row sees are zeros
-          if (r < BN && v < pg.n && pg.any(pg.page(v) * 16 + (r & 15))) {
-            const uint8_t* rec = raw + (r >> 4) * F::kRecord;
-            code[k] = *reinterpret_cast<const uint4*>(rec + (r & 15) * F::kRowBytes + gi * 16);
-            pair[k] = *reinterpret_cast<const uint32_t*>(rec + F::kPairs + ((r & 15) * G + gi) * 4);
-          }
-        }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sm.raw_empty[rpos]);
-        if (use > 0 && !warp_wait(&sm.empty[pos], (use - 1) & 1, &sm.abort, lane)) {
-          if (lane == 0) note_abort(sm, a.err);
-          break;
-        }
-#pragma unroll
-        for (int k = 0; k < MINE; ++k) {
-          const int r = (p0 + k * kDequantWarps) * KEYS + rk;
-          if (r >= BN) break;
-          const uint32_t y0 = (x & 1) ? code[k].y : code[k].x, y1 = (x & 1) ? code[k].x : code[k].y;
-          const uint32_t y2 = (x & 1) ? code[k].w : code[k].z, y3 = (x & 1) ? code[k].z : code[k].w;
-          const uint32_t words[4] = {(x & 2) ? y2 : y0, (x & 2) ? y3 : y1, (x & 2) ? y0 : y2, (x & 2) ? y1 : y3};
-          uint8_t* dst = sm.kv[pos] + row_offset<D>(r, gi >> 1);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            __half2 h[4];
-            q4_values(words[w], *reinterpret_cast<const __half2*>(&pair[k]), h);
-            *reinterpret_cast<uint4*>(dst + ((((gi & 1) * 4 + (w ^ x)) ^ (r & 7)) << 4)) =
-                make_uint4(*reinterpret_cast<uint32_t*>(&h[0]), *reinterpret_cast<uint32_t*>(&h[1]),
-                           *reinterpret_cast<uint32_t*>(&h[2]), *reinterpret_cast<uint32_t*>(&h[3]));
-          }
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sm.full[pos]);
-      }
-    } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA issuer
-      if (lane == 0 && n > 0) {
-        const uint32_t kv_base = ptx::smem_u32(sm.kv[0]);
-        bool ok = ptx::mbar_wait(&sm.q_full, 0, &sm.abort, kWaitLimitNs);
-        ptx::tc_fence_after();
-        auto slot_ready = [&](int idx) -> bool {
-          if (!ptx::mbar_wait(&sm.full[idx % C::NSLOT], (idx / C::NSLOT) & 1, &sm.abort, kWaitLimitNs)) return false;
-          ptx::tc_fence_after();
-          return true;
-        };
-        const uint64_t q_desc[2] = {ptx::smem_desc(ptx::smem_u32(sm.q[0]), 16, 1024, 2),
-                                    ptx::smem_desc(ptx::smem_u32(sm.q[1]), 16, 1024, 2)};
-        const uint64_t k_desc = ptx::smem_desc(kv_base, 16, C::GS, 2);
-        const uint64_t v_desc = ptx::smem_desc(kv_base, 1024, C::GS, 2);
-        auto qk = [&](int w, int j) {
-          const uint64_t kd = ptx::desc_add(k_desc, (uint32_t)(((2 * j) % C::NSLOT) * C::TILE) >> 4);
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            ptx::mma_ss(tmem + 128 * w, ptx::desc_add(q_desc[w], ((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4),
-                        ptx::desc_add(kd, ((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), IDESC_QK, ks > 0);
-          ptx::mma_commit(&sm.s_full[w]);
-        };
-        auto pv = [&](int w, int j) {
-          const uint64_t vd = ptx::desc_add(v_desc, (uint32_t)(((2 * j + 1) % C::NSLOT) * C::TILE) >> 4);
-#pragma unroll
-          for (int ks = 0; ks < BN / 16; ++ks)
-            ptx::mma_ts(tmem + O_COL[w], tmem + 128 * w + ks * 8, ptx::desc_add(vd, (ks * 2 * C::GS) >> 4), IDESC_PV,
-                        (j > 0 || ks > 0) ? 1u : 0u);
-        };
-        if (ok) ok = slot_ready(0);
-        if (ok)
-          for (int w = 0; w < n_q; ++w) qk(w, 0);
-        for (int j = 0; ok && j < n; ++j) {
-          const bool next = j + 1 < n;
-          if (!slot_ready(2 * j + 1)) {
+      while (next_item()) {
+        const Item& it = sm.info[seq & 1];
+        const int n = it.n, t_begin = it.t_begin;
+        const WinPages pg = it.pg;
+        bool ok = true;
+        for (int i = 0; i < 2 * n; ++i) {
+          if (__any_sync(0xffffffffu, *(volatile int*)&sm.abort != 0)) {
             ok = false;
             break;
           }
-          for (int w = 0; w < n_q && ok; ++w) {
-            if (!ptx::mbar_wait(&sm.p_full[w], j & 1, &sm.abort, kWaitLimitNs)) {
+          const int idx = 2 * tb + i;
+          const int pos = idx % C::NSLOT, use = idx / C::NSLOT, rpos = idx % 3;
+          if (!warp_wait(&sm.raw_full[rpos], (idx / 3) & 1, &sm.abort, lane)) {
+            if (lane == 0) note_abort(sm, a.err);
+            ok = false;
+            break;
+          }
+          // All of the warp's codes first: the reads overlap each other and the wait for the slot.
+          const uint8_t* raw = sm.raw[POOLQ4 ? rpos : 0];
+          const int p0 = (pw + idx) % kDequantWarps;
+          uint4 code[MINE];
+          uint32_t pair[MINE];
+#pragma unroll
+          for (int k = 0; k < MINE; ++k) {
+            const int r = (p0 + k * kDequantWarps) * KEYS + rk;  // key of the tile
+            const int v = kPages * (t_begin + (i >> 1)) + (r >> 4);
+            code[k] = make_uint4(0, 0, 0, 0);
+            pair[k] = 0;  // keys that no row sees are zeros
+            if (r < BN && v < pg.n && pg.any(pg.page(v) * 16 + (r & 15))) {
+              const uint8_t* rec = raw + (r >> 4) * F::kRecord;
+              code[k] = *reinterpret_cast<const uint4*>(rec + (r & 15) * F::kRowBytes + gi * 16);
+              pair[k] = *reinterpret_cast<const uint32_t*>(rec + F::kPairs + ((r & 15) * G + gi) * 4);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sm.raw_empty[rpos]);
+          if (use > 0 && !warp_wait(&sm.empty[pos], (use - 1) & 1, &sm.abort, lane)) {
+            if (lane == 0) note_abort(sm, a.err);
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int k = 0; k < MINE; ++k) {
+            const int r = (p0 + k * kDequantWarps) * KEYS + rk;
+            if (r >= BN) break;
+            const uint32_t y0 = (x & 1) ? code[k].y : code[k].x, y1 = (x & 1) ? code[k].x : code[k].y;
+            const uint32_t y2 = (x & 1) ? code[k].w : code[k].z, y3 = (x & 1) ? code[k].z : code[k].w;
+            const uint32_t words[4] = {(x & 2) ? y2 : y0, (x & 2) ? y3 : y1, (x & 2) ? y0 : y2, (x & 2) ? y1 : y3};
+            uint8_t* dst = sm.kv[pos] + row_offset<D>(r, gi >> 1);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              __half2 h[4];
+              q4_values(words[w], *reinterpret_cast<const __half2*>(&pair[k]), h);
+              *reinterpret_cast<uint4*>(dst + ((((gi & 1) * 4 + (w ^ x)) ^ (r & 7)) << 4)) =
+                  make_uint4(*reinterpret_cast<uint32_t*>(&h[0]), *reinterpret_cast<uint32_t*>(&h[1]),
+                             *reinterpret_cast<uint32_t*>(&h[2]), *reinterpret_cast<uint32_t*>(&h[3]));
+            }
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sm.full[pos]);
+        }
+        if (!ok) break;
+        tb += n;
+        done_item();
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer (lane 0; the warp walks the items together)
+      const uint32_t kv_base = ptx::smem_u32(sm.kv[0]);
+      const uint64_t q_desc[2] = {ptx::smem_desc(ptx::smem_u32(sm.q[0]), 16, 1024, 2),
+                                  ptx::smem_desc(ptx::smem_u32(sm.q[1]), 16, 1024, 2)};
+      const uint64_t k_desc = ptx::smem_desc(kv_base, 16, C::GS, 2);
+      const uint64_t v_desc = ptx::smem_desc(kv_base, 1024, C::GS, 2);
+      int qc[2] = {0, 0}, pc[2] = {0, 0}, oc[2] = {0, 0};  // phases of q_full, p_full, o_full
+      int kpos = 0, kphase = 0;  // ring slot of the next key tile, and the phase that fills it
+      bool ok = true, primed = false;  // primed: tile 0's first scores of this item are under way
+      while (next_item()) {
+        const int n = sm.info[seq & 1].n, n_q = sm.info[seq & 1].n_q;
+        if (lane == 0 && n > 0) {
+          auto ready = [&](int pos, int phase) -> bool {
+            if (!ptx::mbar_wait(&sm.full[pos], phase, &sm.abort, kWaitLimitNs)) return false;
+            ptx::tc_fence_after();
+            return true;
+          };
+          auto qk = [&](int w, uint64_t kd) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+              ptx::mma_ss(tmem + 128 * w, ptx::desc_add(q_desc[w], ((ks >> 2) * (BM * 128) + (ks & 3) * 32) >> 4),
+                          ptx::desc_add(kd, ((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), IDESC_QK, ks > 0);
+            ptx::mma_commit(&sm.s_full[w]);
+          };
+          auto pv = [&](int w, uint64_t vd, uint32_t more) {
+#pragma unroll
+            for (int ks = 0; ks < BN / 16; ++ks)
+              ptx::mma_ts(tmem + O_COL[w], tmem + 128 * w + ks * 8, ptx::desc_add(vd, (ks * 2 * C::GS) >> 4), IDESC_PV,
+                          ks > 0 ? 1u : more);
+          };
+          // The slots of this tile's values and the next tile's keys are worked out before the probabilities are waited
+          // for: from then on every instruction delays the tensor core.
+          ok = ready(kpos, kphase);
+          for (int w = primed ? 1 : 0; w < n_q && ok; ++w) {
+            ok = ptx::mbar_wait(&sm.q_full[w], qc[w] & 1, &sm.abort, kWaitLimitNs);
+            ptx::tc_fence_after();
+            ++qc[w];
+            if (ok) qk(w, ptx::desc_add(k_desc, (uint32_t)(kpos * C::TILE) >> 4));
+          }
+          primed = false;
+          for (int j = 0; ok && j < n; ++j) {
+            const bool next = j + 1 < n;
+            int vpos = kpos + 1, vphase = kphase;
+            if (vpos == C::NSLOT) vpos = 0, vphase ^= 1;
+            kpos += 2;
+            if (kpos >= C::NSLOT) kpos -= C::NSLOT, kphase ^= 1;  // the next key tile's, of this item or the next
+            const uint64_t vd = ptx::desc_add(v_desc, (uint32_t)(vpos * C::TILE) >> 4);
+            const uint64_t kd = ptx::desc_add(k_desc, (uint32_t)(kpos * C::TILE) >> 4);
+            if (!ready(vpos, vphase)) {
               ok = false;
               break;
             }
-            ptx::tc_fence_after();
-            pv(w, j);
-            if (next) {
-              if (w == 0 && !slot_ready(2 * j + 2)) {
+            for (int w = 0; w < n_q && ok; ++w) {
+              if (!ptx::mbar_wait(&sm.p_full[w], pc[w] & 1, &sm.abort, kWaitLimitNs)) {
                 ok = false;
                 break;
               }
-              qk(w, j + 1);
+              ptx::tc_fence_after();
+              pv(w, vd, j > 0 ? 1u : 0u);
+              ++pc[w];
+              if (next) {
+                if (w == 0 && !ready(kpos, kphase)) {
+                  ok = false;
+                  break;
+                }
+                qk(w, kd);
+                continue;
+              }
+              ptx::mma_commit(&sm.o_full[w]);
+              ++oc[w];
+              // While tile 1's softmax still works on this item, tile 0's scores of the next one, if all is in place.
+              if (w == 0 && n_q == 2 && ptx::mbar_try_wait(&sm.info_full[(seq + 1) & 1], ((seq + 1) >> 1) & 1) &&
+                  sm.info[(seq + 1) & 1].n > 0 && ptx::mbar_try_wait(&sm.q_full[0], qc[0] & 1) &&
+                  ptx::mbar_try_wait(&sm.full[kpos], kphase)) {
+                ptx::tc_fence_after();
+                ++qc[0];
+                qk(0, kd);
+                primed = true;
+              }
             }
           }
+          if (!ok) {
+            note_abort(sm, a.err);
+            ptx::mma_commit(&sm.o_full[0]);
+            ++oc[0];
+          }
         }
-        if (!ok) note_abort(sm, a.err);
-        ptx::mma_commit(&sm.mma_done);
-        int dummy = 0;
-        ptx::mbar_wait(&sm.mma_done, 0, &dummy, kWaitLimitNs);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tb += n;
+        done_item();
+      }
+      if (lane == 0) {
+        int never = 0;  // everything issued must finish before TMEM is released
+        for (int w = 0; w < 2; ++w)
+          if (oc[w] > 0) ptx::mbar_wait(&sm.o_full[w], (oc[w] - 1) & 1, &never, kWaitLimitNs);
       }
     }
   } else {
     ptx::regs_inc<Roles<POOLQ4>::kHigh>();
-    if (grp < n_q) {
-      // ------------------------------------------------------------ softmax rows of tile grp
-      const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-      const uint32_t S_COL = 128 * grp;
-      const int p = valid ? base + tok : -1;
-      // The warp's rows with queries are consecutive positions [p_lo, p_hi].
-      const int w_first = i0 + grp * TM + (quarter * 32) / g;
-      int w_last = i0 + grp * TM + (quarter * 32 + 31 < TM * g ? quarter * 32 + 31 : TM * g - 1) / g;
-      w_last = w_last < row.Sq ? w_last : row.Sq - 1;
-      const int p_lo = base + w_first, p_hi = base + w_last;
-      float m_ref = -INFINITY, l = 0.f;
-      bool ok = true;
-      for (int j = 0; j < n; ++j) {
-        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sm.s_full[grp], j & 1, &sm.abort, kWaitLimitNs))) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        // The last group's scores of tile j are committed after every earlier MMA: key tile j and value tile j-1
-        // are no longer read.
-        if (grp == n_q - 1 && trow == 0) {
-          ptx::mbar_arrive(&sm.empty[(2 * j) % C::NSLOT]);
-          if (j > 0) ptx::mbar_arrive(&sm.empty[(2 * j - 1) % C::NSLOT]);
-        }
-        float s[BN];
-        {
-          uint32_t r[BN / 32][32];
+    // ------------------------------------------------------------ softmax: warps 4-7 rows of tile 0, warps 8-11 of tile 1
+    const int grp = warp >= 8 ? 1 : 0, quarter = warp & 3;
+    const int trow = quarter * 32 + lane;  // row of the tile
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t S_COL = 128 * grp;
+    int sc = 0, oc = 0;   // phases of s_full[grp], o_full[grp]
+    int staged = -1;      // (row 0) the slot that the last item's output leaves through
+    auto release_staged = [&]() {
+      if (staged < 0) return;
+      ptx::bulk_wait_read_all();
+      ptx::mbar_arrive(&sm.empty[staged]);
+      staged = -1;
+    };
+    while (next_item()) {
+      const Item& it = sm.info[seq & 1];
+      // (The item is read from shared memory where it is used: the scores need the registers.)
+      if (grp < it.n_q) {
+        const int tok = it.i0 + grp * TM + trow / g;  // local query token of the row
+        const bool valid = trow < TM * g && tok < it.Sq;
+        const bool releases = grp == it.n_q - 1 && trow == 0;
+        float sl2 = a.scale * 1.4426950408889634f;
+        if (POOLQ4 && it.n > 0) {
+          // The row's Q in fp16, scaled so that its largest magnitude lies in [2^13, 2^14).  (Its place is free: this
+          // tile's scores of the last item were seen to be complete.)
+          const int64_t at = (((int64_t)it.q0 + tok) * a.Hq + it.kvh * g + trow % g) * D;
+          const uint4* src = reinterpret_cast<const uint4*>((const T*)a.q + at);
+          uint4 x[D / 8];
 #pragma unroll
-          for (int c = 0; c < BN / 32; ++c) ptx::tmem_ld32(tmem + lane_base + S_COL + c * 32, r[c]);
-          ptx::tmem_wait_ld();
+          for (int v = 0; v < D / 8; ++v) x[v] = valid ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
+          float top = 0.f;
 #pragma unroll
-          for (int c = 0; c < BN / 32; ++c) {
-            ptx::reg_fence32(r[c]);
+          for (int v = 0; v < D / 8; ++v) {
+            const T* e = reinterpret_cast<const T*>(&x[v]);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(r[c][e]);
+            for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(pkv_to_f32<T>(e[c])));
           }
-        }
-        // Whole tile seen by all of the warp's rows?  (Pages of a tile ascend.)
-        const int v0 = kPages * (t_begin + j);
-        const int j_first = pg.page(v0) * 16;
-        const int j_last = v0 + kPages <= pg.n ? pg.page(v0 + kPages - 1) * 16 + 15 : 0x7fffffff;
-        if (!(j_last <= p_lo && (a.window == 0 || j_last < a.sinks || p_hi - j_first < a.window))) {
+          const int e2 = top > 0.f && top <= 3.402823466e38f ? min(13 - ilogbf(top), 64) : 0;
+          sl2 = scalbnf(sl2, -e2);
 #pragma unroll
-          for (int k = 0; k < kPages; ++k) {
-            // Column c of the page is seen when c <= hi and (c < sk or c > lo): a 16-bit mask by shifts.
-            unsigned bits = 0;
-            if (v0 + k < pg.n) {
-              const int j0 = pg.page(v0 + k) * 16;
-              const int hi = p - j0, sk = a.sinks - j0, lo = hi - a.window;
-              bits = hi < 0 ? 0u : hi >= 15 ? 0xffffu : (2u << hi) - 1u;
-              if (a.window) {
-                const unsigned head = sk <= 0 ? 0u : sk >= 16 ? 0xffffu : (1u << sk) - 1u;
-                const unsigned tail = lo < 0 ? 0xffffu : lo >= 15 ? 0u : ~((2u << lo) - 1u);
-                bits &= head | tail;
+          for (int v = 0; v < D / 8; ++v) {
+            const T* e = reinterpret_cast<const T*>(&x[v]);
+            uint32_t w[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              w[c] = ptx::pack_f16x2(scalbnf(pkv_to_f32<T>(e[c]), e2), scalbnf(pkv_to_f32<T>(e[c + 4]), e2));
+            *reinterpret_cast<uint4*>(sm.q[grp] + (v >> 3) * (BM * 128) + trow * 128 + (((v & 7) ^ (trow & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive(&sm.q_full[grp]);
+        }
+        const int p = valid ? it.base + tok : -1;
+        // The warp's rows with queries are consecutive positions [p_lo, p_hi].
+        int w_last = it.i0 + grp * TM + (quarter * 32 + 31 < TM * g ? quarter * 32 + 31 : TM * g - 1) / g;
+        w_last = w_last < it.Sq ? w_last : it.Sq - 1;
+        const int p_lo = it.base + it.i0 + grp * TM + (quarter * 32) / g, p_hi = it.base + w_last;
+        float m_ref = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < it.n; ++j) {
+          if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sm.s_full[grp], sc & 1, &sm.abort, kWaitLimitNs))) {
+            ok = false;
+            break;
+          }
+          ++sc;
+          if (trow == 0) release_staged();
+          ptx::tc_fence_after();
+          // The last group's scores of tile j are committed after every earlier MMA: key tile j and value tile j-1
+          // are no longer read.  (The last tile's two slots stage the output.)
+          if (releases) {
+            const int idx = 2 * (tb + j);
+            if (j < it.n - 1 || n_cta > 1) ptx::mbar_arrive(&sm.empty[idx % C::NSLOT]);
+            if (j > 0) ptx::mbar_arrive(&sm.empty[(idx - 1) % C::NSLOT]);
+          }
+          if (!POOLQ4 && trow == 0 && j == it.n - 1) ptx::mbar_arrive(&sm.q_empty[grp]);
+          float s[BN];
+          {
+            uint32_t r[BN / 32][32];
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) ptx::tmem_ld32(tmem + lane_base + S_COL + c * 32, r[c]);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) {
+              ptx::reg_fence32(r[c]);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[c * 32 + e] = __uint_as_float(r[c][e]);
+            }
+          }
+          // Whole tile seen by all of the warp's rows?  (Pages of a tile ascend.)
+          const int v0 = kPages * (it.t_begin + j);
+          const int j_first = it.pg.page(v0) * 16;
+          const int j_last = v0 + kPages <= it.pg.n ? it.pg.page(v0 + kPages - 1) * 16 + 15 : 0x7fffffff;
+          if (!(j_last <= p_lo && (a.window == 0 || j_last < a.sinks || p_hi - j_first < a.window))) {
+            uint32_t bits[BN / 32];  // seen columns
+            if (v0 >= it.pg.n_sink && (a.window == 0 || j_first >= a.sinks)) {
+              // Consecutive pages past the sinks: columns (p - window, p] - j_first.
+              const int hi = p - j_first, lo = a.window ? hi - a.window : -1;
+#pragma unroll
+              for (int q = 0; q < BN / 32; ++q) {
+                const int h = hi - 32 * q, w = lo - 32 * q;
+                const uint32_t up = h < 0 ? 0u : h >= 31 ? 0xffffffffu : (2u << h) - 1u;
+                const uint32_t down = w < 0 ? 0u : w >= 31 ? 0xffffffffu : (2u << w) - 1u;
+                bits[q] = up & ~down;
+              }
+            } else {
+              // Column c of a page is seen when c <= hi and (c < sk or c > lo); two pages a word.
+#pragma unroll
+              for (int q = 0; q < BN / 32; ++q) {
+                bits[q] = 0;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const int v = v0 + 2 * q + k, j0 = it.pg.page(v) * 16;
+                  const int hi = v < it.pg.n ? p - j0 : -1, sk = a.sinks - j0, lo = p - j0 - a.window;
+                  unsigned b16 = hi < 0 ? 0u : hi >= 15 ? 0xffffu : (2u << hi) - 1u;
+                  if (a.window) {
+                    const unsigned head = sk <= 0 ? 0u : sk >= 16 ? 0xffffu : (1u << sk) - 1u;
+                    const unsigned tail = lo < 0 ? 0xffffu : lo >= 15 ? 0u : ~((2u << lo) - 1u);
+                    b16 &= head | tail;
+                  }
+                  bits[q] |= (b16 & 0xffffu) << (16 * k);
+                }
               }
             }
 #pragma unroll
-            for (int c = 0; c < 16; ++c) s[k * 16 + c] = (bits >> c) & 1 ? s[k * 16 + c] : -INFINITY;
+            for (int c = 0; c < BN; ++c) s[c] = (bits[c >> 5] & (1u << (c & 31))) ? s[c] : -INFINITY;
           }
-        }
-        float mx[8];
+          float mx[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) mx[u] = fmaxf(s[2 * u], s[2 * u + 1]);
+          for (int u = 0; u < 8; ++u) mx[u] = fmaxf(s[2 * u], s[2 * u + 1]);
 #pragma unroll
-        for (int c = 16; c < BN; c += 16)
+          for (int c = 16; c < BN; c += 16)
 #pragma unroll
-          for (int u = 0; u < 8; ++u) mx[u] = ptx::max3(mx[u], s[c + 2 * u], s[c + 2 * u + 1]);
-        const float m_tile =
-            fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * sl2;
-        const bool need = m_tile > m_ref + kRescale;
-        const bool rescale = __any_sync(0xffffffffu, need);
-        const float alpha = need ? ptx::ex2(m_ref - m_tile) : 1.f;  // 0 on a row's first visible tile
-        if (need) {
-          l *= alpha;
-          m_ref = m_tile;
-        }
-        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll
-        for (int c = 0; c < BN / 64; ++c) {
-          uint32_t r[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float x0, x1;
-            ptx::fma2(x0, x1, s[c * 64 + 2 * e], s[c * 64 + 2 * e + 1], sl2, sl2, -mu, -mu);
-            const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
-            if (e & 1)
-              ptx::add2(l2, l3, p0, p1);
-            else
-              ptx::add2(l0, l1, p0, p1);
-            r[e] = OPBF16 ? ptx::pack_bf16x2(p0, p1) : ptx::pack_f16x2(p0, p1);
+            for (int u = 0; u < 8; ++u) mx[u] = ptx::max3(mx[u], s[c + 2 * u], s[c + 2 * u + 1]);
+          const float m_tile =
+              fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) *
+              sl2;
+          const bool need = m_tile > m_ref + kRescale;
+          const bool rescale = __any_sync(0xffffffffu, need);
+          const float alpha = need ? ptx::ex2(m_ref - m_tile) : 1.f;  // 0 on a row's first visible tile
+          if (need) {
+            l *= alpha;
+            m_ref = m_tile;
           }
-          ptx::tmem_st32(tmem + lane_base + S_COL + c * 32, r);
-        }
-        l += (l0 + l1) + (l2 + l3);
-        if (rescale && j > 0) {
+          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+          float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < BN / 64; ++c) {
             uint32_t r[32];
-            ptx::tmem_ld32(tmem + lane_base + O_COL[grp] + c * 32, r);
-            ptx::tmem_wait_ld();
-            ptx::reg_fence32(r);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-            ptx::tmem_st32(tmem + lane_base + O_COL[grp] + c * 32, r);
-          }
-        }
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(&sm.p_full[grp]);
-      }
-      if (!ok) note_abort(sm, a.err);
-
-      // ---------------------------------------------------------------- epilogue
-      float o[D];
-#pragma unroll
-      for (int c = 0; c < D; ++c) o[c] = 0.f;
-      if (ok && n > 0) {
-        if (__all_sync(0xffffffffu, ptx::mbar_wait(&sm.mma_done, 0, &sm.abort, kWaitLimitNs))) {
-          ptx::tc_fence_after();
-          uint32_t r[D / 32][32];
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) ptx::tmem_ld32(tmem + lane_base + O_COL[grp] + c * 32, r[c]);
-          ptx::tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            ptx::reg_fence32(r[c]);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              // 4-bit values come in the order of channels (0, 4, 1, 5, 2, 6, 3, 7) of each eight
-              const int ch = POOLQ4 ? (c * 32 + (e & ~7)) + ((e & 1) * 4 + ((e >> 1) & 3)) : c * 32 + e;
-              o[ch] = __uint_as_float(r[c][e]);
+              float x0, x1;
+              ptx::fma2(x0, x1, s[c * 64 + 2 * e], s[c * 64 + 2 * e + 1], sl2, sl2, -mu, -mu);
+              const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+              if (e & 1)
+                ptx::add2(l2, l3, p0, p1);
+              else
+                ptx::add2(l0, l1, p0, p1);
+              r[e] = OPBF16 ? ptx::pack_bf16x2(p0, p1) : ptx::pack_f16x2(p0, p1);
+            }
+            ptx::tmem_st32(tmem + lane_base + S_COL + c * 32, r);
+          }
+          l += (l0 + l1) + (l2 + l3);
+          if (rescale && j > 0) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t r[32];
+              ptx::tmem_ld32(tmem + lane_base + O_COL[grp] + c * 32, r);
+              ptx::tmem_wait_ld();
+              ptx::reg_fence32(r);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+              ptx::tmem_st32(tmem + lane_base + O_COL[grp] + c * 32, r);
             }
           }
-        } else {
-          note_abort(sm, a.err);
-          ok = false;
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&sm.p_full[grp]);
         }
-      }
-      if (n_cta > 1) {
-        // Staged for the merge in the key/value ring and the Q buffer, which no copy or MMA uses any more.
-        float* st = reinterpret_cast<float*>(sm.kv[0]) + (grp * BM + trow) * C::OSTRIDE;
+
+        // ---------------------------------------------------------------- epilogue
+        float o[D];
 #pragma unroll
-        for (int v = 0; v < D / 4; ++v)
-          *reinterpret_cast<float4*>(st + 4 * v) = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-        float* ml = reinterpret_cast<float*>(sm.q[0]);  // [2 BM] maxima, [2 BM] sums
-        ml[grp * BM + trow] = m_ref;
-        ml[2 * BM + grp * BM + trow] = l;
-      } else {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint32_t w[D / 2];
+        for (int c = 0; c < D; ++c) o[c] = 0.f;
+        if (ok && it.n > 0) {
+          if (__all_sync(0xffffffffu, ptx::mbar_wait(&sm.o_full[grp], oc & 1, &sm.abort, kWaitLimitNs))) {
+            ptx::tc_fence_after();
+            uint32_t r[D / 32][32];
 #pragma unroll
-        for (int c = 0; c < D / 2; ++c) {
-          const float x0 = o[2 * c] * inv, x1 = o[2 * c + 1] * inv;
-          w[c] = OUTBF16 ? ptx::pack_bf16x2(x0, x1) : ptx::pack_f16x2(x0, x1);
-        }
-        // A whole tile leaves through shared memory (the Q buffer, free once every MMA is done) and one TMA store
-        // per column half; a tile with fewer tokens stores per thread.
-        const bool staged = n > 0 && i0 + (grp + 1) * TM <= row.Sq;
-        if (staged) {
-          uint8_t* tile = sm.q[grp];
+            for (int c = 0; c < D / 32; ++c) ptx::tmem_ld32(tmem + lane_base + O_COL[grp] + c * 32, r[c]);
+            ptx::tmem_wait_ld();
 #pragma unroll
-          for (int v = 0; v < D / 8; ++v)
-            *reinterpret_cast<uint4*>(tile + (v >> 3) * (BM * 128) + trow * 128 + (((v & 7) ^ (trow & 7)) << 4)) =
-                make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
-          ptx::fence_proxy_async_smem();
-          asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(BM) : "memory");
-          if (trow == 0 && !*(volatile int*)&sm.abort) {
+            for (int c = 0; c < D / 32; ++c) {
+              ptx::reg_fence32(r[c]);
 #pragma unroll
-            for (int dh = 0; dh < D / 64; ++dh)
-              tma_store_4d(&maps.o, dh * 64, 0, kvh, row.q0 + i0 + grp * TM, tile + dh * (BM * 128));
-            ptx::bulk_commit();
-            ptx::bulk_wait_read_all();
+              for (int e = 0; e < 32; ++e) {
+                // 4-bit values come in the order of channels (0, 4, 1, 5, 2, 6, 3, 7) of each eight
+                const int ch = POOLQ4 ? (c * 32 + (e & ~7)) + ((e & 1) * 4 + ((e >> 1) & 3)) : c * 32 + e;
+                o[ch] = __uint_as_float(r[c][e]);
+              }
+            }
+            ++oc;
+            ptx::tc_fence_before();  // read before the next item's first P.V
+          } else {
+            ok = false;
           }
-        } else if (valid && ok) {
-          uint4* dst =
-              reinterpret_cast<uint4*>((T*)a.out + (((int64_t)row.q0 + tok) * a.Hq + kvh * g + trow % g) * D);
+        }
+        if (!ok) {
+          note_abort(sm, a.err);
+          break;
+        }
+        if (n_cta > 1) {
+          // Staged for the merge in the key/value ring and the Q buffer, which no copy or MMA uses any more once the
+          // other tile's output is complete too (a cluster has one item).
+          if (it.n > 0 && it.n_q == 2 &&
+              !__all_sync(0xffffffffu, ptx::mbar_wait(&sm.o_full[grp ^ 1], 0, &sm.abort, kWaitLimitNs))) {
+            note_abort(sm, a.err);
+            break;
+          }
+          float* st = reinterpret_cast<float*>(sm.kv[0]) + (grp * BM + trow) * C::OSTRIDE;
 #pragma unroll
-          for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+          for (int v = 0; v < D / 4; ++v)
+            *reinterpret_cast<float4*>(st + 4 * v) = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+          float* ml = reinterpret_cast<float*>(sm.q[0]);  // [2 BM] maxima, [2 BM] sums
+          ml[grp * BM + trow] = m_ref;
+          ml[2 * BM + grp * BM + trow] = l;
+        } else {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          uint32_t w[D / 2];
+#pragma unroll
+          for (int c = 0; c < D / 2; ++c) {
+            const float x0 = o[2 * c] * inv, x1 = o[2 * c + 1] * inv;
+            w[c] = OUTBF16 ? ptx::pack_bf16x2(x0, x1) : ptx::pack_f16x2(x0, x1);
+          }
+          T* const out = (T*)a.out + ((int64_t)it.q0 * a.Hq + it.kvh * g) * D;
+          if (it.n > 0) {
+            // Through shared memory -- the last tile's key slot (tile 0) and value slot (tile 1), which no MMA reads any
+            // more -- because rows stored thread by thread take an instruction 32 lines: 7000 cycles a tile.
+            const int slot = (2 * (tb + it.n) - 2 + grp) % C::NSLOT;
+            uint8_t* tile = sm.kv[slot];  // [D/64][128 rows][128 B], swizzled like Q
+            if (releases && grp == 0) ptx::mbar_arrive(&sm.empty[(slot + 1) % C::NSLOT]);  // nothing to stage of tile 1
+#pragma unroll
+            for (int v = 0; v < D / 8; ++v)
+              *reinterpret_cast<uint4*>(tile + (v >> 3) * (BM * 128) + trow * 128 + (((v & 7) ^ (trow & 7)) << 4)) =
+                  make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+            const int first = it.i0 + grp * TM;
+            if (first + TM <= it.Sq) {  // whole tiles: one TMA store per column half
+              ptx::fence_proxy_async_smem();
+              asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(BM) : "memory");
+              if (trow == 0) {
+#pragma unroll
+                for (int dh = 0; dh < D / 64; ++dh)
+                  tma_store_4d(&maps.o, dh * 64, 0, it.kvh, it.q0 + first, tile + dh * (BM * 128));
+                ptx::bulk_commit();
+                staged = slot;  // given back once it has been read: when the next item's first scores are there
+              }
+            } else {  // a sequence's last tile: the rows that are queries
+              asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(BM) : "memory");
+              const int rows = (it.Sq - first) * g;
+              for (int e = trow; e < rows * (D / 8); e += BM) {
+                const int r = e / (D / 8), v = e % (D / 8);
+                reinterpret_cast<uint4*>(out + ((int64_t)(first + r / g) * a.Hq + r % g) * D)[v] =
+                    *reinterpret_cast<const uint4*>(tile + (v >> 3) * (BM * 128) + r * 128 + (((v & 7) ^ (r & 7)) << 4));
+              }
+              asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(BM) : "memory");
+              if (trow == 0) ptx::mbar_arrive(&sm.empty[slot]);
+            }
+          } else if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(out + ((int64_t)tok * a.Hq + trow % g) * D);
+#pragma unroll
+            for (int v = 0; v < D / 8; ++v) dst[v] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+          }
         }
       }
+      if (trow == 0 && (it.n == 0 || grp >= it.n_q)) release_staged();  // no first tile here to do it after
+      tb += it.n;
+      done_item();
     }
+    if (trow == 0) release_staged();  // read before the shared memory goes away
   }
 
   // ---------------------------------------------------------------- teardown, and the cluster's merge
+  __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, kTmemCols);
   }
-  if (n_cta > 1) {
+  if (n_cta > 1 && sm.info[0].n >= 0) {  // the same for every CTA of the cluster
+    const Item& it = sm.info[0];
     __syncwarp();
     cluster_sync();
     // Rows r of tile t in turn over the cluster's warps; a lane takes D/32 channels.
     constexpr int CH = D / 32;
-    const int rows = n_q * BM;
+    const int rows = it.n_q * BM;
     for (int e = (int)rank * (kThreads / 32) + warp; e < rows; e += (int)n_cta * (kThreads / 32)) {
       const int tr = e % BM;
-      const int tk = i0 + (e / BM) * TM + tr / g;
-      if (tr >= TM * g || tk >= row.Sq) continue;
+      const int tk = it.i0 + (e / BM) * TM + tr / g;
+      if (tr >= TM * g || tk >= it.Sq) continue;
       float mk = -INFINITY, lk = 0.f;
       if (lane < (int)n_cta) {
         const uint32_t ml = cluster_addr(reinterpret_cast<float*>(sm.q[0]) + e, lane);
@@ -686,7 +1002,7 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
         }
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      T* dst = (T*)a.out + (((int64_t)row.q0 + tk) * a.Hq + kvh * g + tr % g) * D + lane * CH;
+      T* dst = (T*)a.out + (((int64_t)it.q0 + tk) * a.Hq + it.kvh * g + tr % g) * D + lane * CH;
 #pragma unroll
       for (int c = 0; c < CH; c += 2) store_pair<T>(dst + c, acc[c] * inv, acc[c + 1] * inv);
     }

@@ -149,12 +149,13 @@ int64_t pkv_visible_keys(const PkvWinArgs& a, int64_t tokens);
 // CTAs (1, 2, 4, 8 or 16) that share one item's `steps` key steps; `rate`: what a step costs each of several CTAs on
 // an SM, times their number, as against one alone; `setup`: a CTA's set-up in steps.
 int pkv_plan_cluster(const PkvKernelState& state, int64_t items, int64_t steps, double rate, double setup);
-// Single CTAs (2 .. 64) that share one item where that is estimated under any cluster; else 1.  `combine`: the cost of
+constexpr int kPkvMaxWinSplits = 64;
+// Single CTAs (2 .. kPkvMaxWinSplits) that share one item where that is estimated under any cluster; else 1.  `combine`: the cost of
 // the launch that merges them, in steps.
 int pkv_plan_splits(const PkvKernelState& state, int64_t items, int64_t steps, double rate, double setup,
                     double combine);
-// For a kernel of one CTA per SM, whose set-up and epilogue cost `fixed` steps: `whole` items run as single CTAs, the others in a second launch of
-// clusters of `ctas` (0 whole items: one launch).
+// For a kernel of one CTA per SM, whose set-up and epilogue cost `fixed` steps: `whole` items run as single CTAs, the
+// others in a second launch of clusters of `ctas` (0 whole items: one launch).
 struct PkvClusterPlan {
   int64_t whole;
   int ctas;

@@ -247,8 +247,9 @@ int pkv_plan_splits(const PkvKernelState& state, int64_t items, int64_t steps, d
   Split best = best_cluster(state, dev, items, steps, rate, setup);
   best.ctas = 1;
   for (int64_t m = 1; m <= per_sm; ++m) {  // as many CTAs on every SM
-    const int64_t n = m * sms / items;
-    if (n < 2 || n > 64 || n > steps) continue;
+    int64_t n = m * sms / items;
+    if (n > kPkvMaxWinSplits) n = kPkvMaxWinSplits;
+    if (n < 2 || n > steps) continue;
     const double cost = shared_cost(items * n, sms, (steps + n - 1) / n, rate, setup) + combine;
     if (cost < 0.99 * best.cost) best = Split{(int)n, cost};
   }

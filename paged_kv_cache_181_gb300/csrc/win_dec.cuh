@@ -12,8 +12,8 @@ namespace dec {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr float kRescale = 8.f;  // log2 units
-// What a CTA's set-up costs and what the combine launch has to gain, in steps (one page per warp): 3 us on the GPU, and 8 us of the host's time (a
-// workspace, a launch), which a stream of short calls waits for.
+// What a CTA's set-up costs and what the combine launch has to gain, in steps (one page per warp): 3 us on the GPU, and
+// 8 us of the host's time (a workspace, a launch), which a stream of short calls waits for.
 constexpr double kSetupSteps = 2.0, kCombineSteps = 8.0;
 
 template <bool BF16>
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(D) combine_kernel(const PkvWinArgs a, const in
   const WinRow row = win_row(a, b, false);
   const int64_t at = (int64_t)qt * ROWS + r;
   if (at >= (int64_t)row.Sq * g) return;
-  __shared__ float sm_w[64];
+  __shared__ float sm_w[kPkvMaxWinSplits];
   __shared__ float2 sm_x[PAIRS];
   __shared__ float sm_sum;
   const int tid = threadIdx.x, lane = tid & 31;

@@ -495,3 +495,13 @@ def test_ordinary_calls_take_the_fast_way(lib, monkeypatch):
     lib.paged_attn_window(q, pool, pool, table, qsl, lens, 3, 64, 0.1, stream=torch.cuda.current_stream())
     lib.paged_attn_q4(q, four, four, table, qsl, lens, 3, 64, 0.1, window=4)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_many_prompt_tiles_in_turn(lib, q4):
+    """More items than SMs, of one and of two query tiles, whole and ragged, with keys and without: what one CTA works
+    through in turn."""
+    rows = [(70, 90), (130, 130), (0, 50), (33, 400), (64, 70), (200, 100), (129, 300)] * 6
+    agree(*attention(lib, rows, 8, 8, 64, "bf16", 45, 3, q4, seed=21, tail=1))
+    rows = [(97, 97), (40, 41), (64, 64), (17, 200), (5, 0)] * 9
+    agree(*attention(lib, rows, 16, 4, 128, "f16", 0, 0, q4, seed=22))
