@@ -20,16 +20,18 @@
 //                 and the output's channels are permuted to match, which is free, instead of the codes.
 // CTAs are persistent: warp 0 asks the hardware for a CTA that has not started yet, cancels its launch and takes its
 // item (clusterlaunchcontrol), and the roles go on to it each at its own pace: the producers load the next item's
-// keys and queries while the softmax warps finish the last one.  4096 tokens x 40 heads over 8 kv heads, D = 128, with a
+// keys and queries while the softmax warps finish the last one.  8192 tokens x 32 heads over 8 kv heads, D = 128, with a
 // window of 64: 46 us instead of 69 with a CTA an item; window 1024: 145 instead of 163.  (Clusters keep to their item.)
 //
-// What bounds it: a tile's chain.  Its probabilities overwrite its scores in TMEM, so each 128 keys take the softmax
-// (1700 cycles of a row's 128 exponentials; masked ones 2800 and more), its products (1024 cycles for both tiles) and
-// the hand-overs one after the other, about 3500 cycles, and only the other tile's work fills the gaps.  The tensor
-// cores reach 1.19 PFLOP/s over 4000-key windows, 1.07 with 4-bit pools, where turning codes into numbers adds to it.
+// What bounds it: a tile's chain.  Its probabilities overwrite its scores in TMEM (two score and two output
+// accumulators fill it at D = 128), so each 128 keys take the softmax (1700 cycles; masked ones 2800 and more), its two
+// products (1024 cycles) and the hand-overs one after the other, 3400 cycles, while only the other tile's products fill
+// the gaps: 1.2 PFLOP/s over 4000-key windows, 1.06 with 4-bit pools, where turning codes into numbers adds to it.
+// Scores of 64 keys that go on by themselves were slower (a TMEM read is mostly latency, and there were twice as many).
 // The order of MMAs, the ring of slots shared by key and value tiles, the lazy rescale and the register split between
 // warpgroups are those of the prefix-mask kernel (attn_tc.cu), which says why.
-// Every mbarrier wait is bounded in time (1 s, or 60 for the next item); on expiry the CTA records PKV_DEVERR_TIMEOUT and unwinds.
+// Every mbarrier wait is bounded in time (1 s, or 60 for the next item); on expiry the CTA records PKV_DEVERR_TIMEOUT
+// and unwinds.
 
 #include <cuda.h>
 
@@ -72,6 +74,9 @@ struct Cfg {
   static constexpr int NRAW = POOLQ4 ? 3 : 0;             // 4-bit tiles in flight
   static constexpr int RAW = kPages * Q4<D>::kRecord;     // one of them
   static constexpr int GS = (D / 64) * 1024;  // stride of 8-row atoms in a key/value tile
+  // The probabilities of a tile are handed over in two parts, so that the products of the first one overlap the
+  // exponentials of the second (2 % over 4000-key windows); with 4-bit pools in one, where two lost 5 %.
+  static constexpr int PARTS = POOLQ4 ? 1 : 2;
   static constexpr int OSTRIDE = D + 4;       // floats between rows staged for the merge
 };
 
@@ -93,7 +98,7 @@ struct alignas(1024) WinSmem {
   uint8_t raw[POOLQ4 ? C::NRAW : 1][POOLQ4 ? C::RAW : 16];  // records of 4-bit tiles
   uint64_t full[C::NSLOT], empty[C::NSLOT];
   uint64_t raw_full[3], raw_empty[3];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];  // p_full: [query tile][part of the keys]
   uint64_t info_full[2], info_empty[2], clc_full;
   alignas(16) uint4 clc;  // the scheduler's last answer
   Item info[2];           // the item in work, and the one to come
@@ -284,7 +289,8 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
     for (int w = 0; w < 2; ++w) {
       ptx::mbar_init(&sm.q_full[w], POOLQ4 ? 128 : 1);
       ptx::mbar_init(&sm.s_full[w], 1);
-      ptx::mbar_init(&sm.p_full[w], 128);
+      ptx::mbar_init(&sm.p_full[w][0], 128);
+      ptx::mbar_init(&sm.p_full[w][1], 128);
       ptx::mbar_init(&sm.q_empty[w], 1);
       ptx::mbar_init(&sm.o_full[w], 1);
       ptx::mbar_init(&sm.info_full[w], 1);
@@ -607,9 +613,9 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
                           ptx::desc_add(kd, ((ks >> 2) * 1024 + (ks & 3) * 32) >> 4), IDESC_QK, ks > 0);
             ptx::mma_commit(&sm.s_full[w]);
           };
-          auto pv = [&](int w, uint64_t vd, uint32_t more) {
+          auto pv = [&](int w, int h, uint64_t vd, uint32_t more) {  // part h of the tile's keys
 #pragma unroll
-            for (int ks = 0; ks < BN / 16; ++ks)
+            for (int ks = h * (BN / 16 / C::PARTS); ks < (h + 1) * (BN / 16 / C::PARTS); ++ks)
               ptx::mma_ts(tmem + O_COL[w], tmem + 128 * w + ks * 8, ptx::desc_add(vd, (ks * 2 * C::GS) >> 4), IDESC_PV,
                           ks > 0 ? 1u : more);
           };
@@ -636,12 +642,16 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
               break;
             }
             for (int w = 0; w < n_q && ok; ++w) {
-              if (!ptx::mbar_wait(&sm.p_full[w], pc[w] & 1, &sm.abort, kWaitLimitNs)) {
-                ok = false;
-                break;
+#pragma unroll
+              for (int h = 0; h < C::PARTS; ++h) {
+                if (!ptx::mbar_wait(&sm.p_full[w][h], pc[w] & 1, &sm.abort, kWaitLimitNs)) {
+                  ok = false;
+                  break;
+                }
+                ptx::tc_fence_after();
+                pv(w, h, vd, j > 0 ? 1u : 0u);
               }
-              ptx::tc_fence_after();
-              pv(w, vd, j > 0 ? 1u : 0u);
+              if (!ok) break;
               ++pc[w];
               if (next) {
                 if (w == 0 && !ready(kpos, kphase)) {
@@ -841,23 +851,25 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
               r[e] = OPBF16 ? ptx::pack_bf16x2(p0, p1) : ptx::pack_f16x2(p0, p1);
             }
             ptx::tmem_st32(tmem + lane_base + S_COL + c * 32, r);
-          }
-          l += (l0 + l1) + (l2 + l3);
-          if (rescale && j > 0) {
+            if (c == 0 && rescale && j > 0) {
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t r[32];
-              ptx::tmem_ld32(tmem + lane_base + O_COL[grp] + c * 32, r);
-              ptx::tmem_wait_ld();
-              ptx::reg_fence32(r);
+              for (int d = 0; d < D / 32; ++d) {
+                uint32_t o[32];
+                ptx::tmem_ld32(tmem + lane_base + O_COL[grp] + d * 32, o);
+                ptx::tmem_wait_ld();
+                ptx::reg_fence32(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-              ptx::tmem_st32(tmem + lane_base + O_COL[grp] + c * 32, r);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                ptx::tmem_st32(tmem + lane_base + O_COL[grp] + d * 32, o);
+              }
+            }
+            if (C::PARTS == 2 || c == 1) {
+              ptx::tmem_wait_st();
+              ptx::tc_fence_before();
+              ptx::mbar_arrive(&sm.p_full[grp][C::PARTS == 2 ? c : 0]);
             }
           }
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(&sm.p_full[grp]);
+          l += (l0 + l1) + (l2 + l3);
         }
 
         // ---------------------------------------------------------------- epilogue
