@@ -601,11 +601,15 @@ def paged_kv_gather_q4(key_pool, value_pool, block_table, stage_k, stage_v, *, f
 
 
 def _scratch(nbytes: int, q, stream):
-    """A workspace from torch's allocator for one call on ``stream`` (None: the current one)."""
-    workspace = _torch().empty(nbytes, dtype=_u8, device=q.device)
-    if stream is not None:
-        workspace.record_stream(stream)
-    return workspace
+    """A workspace from torch's allocator for one call on ``stream`` (None: the current one).
+
+    It is allocated as that stream's: memory of the current one could still be read by work queued there.
+    """
+    torch = _torch()
+    if stream is None:
+        return torch.empty(nbytes, dtype=_u8, device=q.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=_u8, device=q.device)
 
 
 def _attn_window(fn: str, entry, q4: bool, q, key_pool, value_pool, block_table, query_start_loc, seq_lens,

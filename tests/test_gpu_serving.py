@@ -505,3 +505,93 @@ def test_many_prompt_tiles_in_turn(lib, q4):
     agree(*attention(lib, rows, 8, 8, 64, "bf16", 45, 3, q4, seed=21, tail=1))
     rows = [(97, 97), (40, 41), (64, 64), (17, 200), (5, 0)] * 9
     agree(*attention(lib, rows, 16, 4, 128, "f16", 0, 0, q4, seed=22))
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_offsets_past_32_bits(lib, q4):
+    """Blocks, query rows and output rows whose byte offsets pass 2^32 (and element offsets 2^31): the same bits as from
+    a small cache."""
+    hq, hkv, d = 16, 8, 128
+    small = 40
+    blocks = (1 << 32) // (10 * d * hkv) + 77 if q4 else (1 << 31) // (16 * hkv * d) + 77
+    lead = (1 << 31) // (hq * d) + 11  # query tokens before the ones of interest
+    g = torch.Generator().manual_seed(5)
+    rows = [(1, 300), (70, 200), (9, 40)]
+    tokens = sum(r[0] for r in rows)
+    fill = torch.randn(3, sum(r[1] for r in rows), hkv, d, generator=g).bfloat16().cuda()
+    q = torch.randn(tokens, hq, d, generator=g).bfloat16().cuda()
+    table, used = sc.table_of(1, [r[1] for r in rows], 19, spare=1)
+    assert used <= small
+    append, attend = ((lib.paged_kv_append_q4, lib.paged_attn_q4) if q4 else (lib.paged_kv_append, lib.paged_attn_window))
+    lens = torch.tensor([r[1] for r in rows], dtype=torch.int32).cuda()
+    slots = np.concatenate([table[b][np.arange(r[1]) // 16].astype(np.int64) * 16 + np.arange(r[1]) % 16
+                            for b, r in enumerate(rows)])
+    cs = torch.randn(512, d, generator=g).cuda()
+    pos = torch.from_numpy(np.concatenate([np.arange(r[1]) for r in rows]).astype(np.int32)).cuda()
+    got = []
+    for n, first in ((small, 0), (blocks, blocks - used)):
+        shape, kind = ((n, hkv, 10 * d), torch.uint8) if q4 else ((n * 16, hkv, d), torch.bfloat16)
+        kp, vp = (torch.empty(shape, dtype=kind, device="cuda") for _ in range(2))
+        tb = torch.from_numpy(np.where(table < used, table + first, table).astype(np.int32)).cuda()
+        append(None, fill[0], fill[1], pos, cs, torch.from_numpy(slots + first * 16).cuda(), kp, vp,
+               flags=lib.PKV_CHECK_BOUNDS)
+        for flags in (0, lib.PKV_FORCE_SIMT):
+            for ahead in (0, lead) if first else (0,):
+                qs = q if not ahead else torch.empty(ahead + tokens, hq, d, dtype=q.dtype, device="cuda")
+                out = torch.zeros_like(qs)
+                if ahead:
+                    qs[ahead:] = q
+                for b, most in ((0, 1), (1, 70), (2, 9)):  # a decode step, a prompt, many rows of one tile
+                    at = ahead + sum(r[0] for r in rows[:b])
+                    qsl = torch.tensor([at, at + rows[b][0]], dtype=torch.int32).cuda()
+                    attend(qs, kp, vp, tb[b:b + 1], qsl, lens[b:b + 1], most, 300, 0.09, window=150, sinks=5, out=out,
+                           flags=flags | lib.PKV_CHECK_BOUNDS)
+                got.append((flags, out[ahead:].clone()))
+                assert ahead == 0 or not out[:ahead].any()
+        assert lib.check() == 0
+        if q4:
+            stage = [torch.empty(3, 19 * 16, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+            for b, r in enumerate(rows):
+                n_blocks = -(-r[1] // 16)
+                lib.paged_kv_gather_q4(kp, vp, tb[b:b + 1], stage[0][b:b + 1], stage[1][b:b + 1], n_blocks=n_blocks)
+                got.append(("stage", torch.stack([s[b, : r[1]] for s in stage])))
+        del kp, vp
+    for what in {w for w, _ in got}:
+        same = [x for w, x in got if w == what]
+        if what == "stage":
+            assert all(torch.equal(a, b) for a, b in zip(same[:3], same[3:]))
+        else:
+            assert len(same) == 3 and all(torch.equal(same[0], x) for x in same[1:]) and same[0].any()
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_seventy_thousand_sequences(lib, q4):
+    """More sequences than a grid's second dimension holds, some without keys, one key or one block each."""
+    B, hq, hkv, d = 70001, 2, 1, 64
+    g = torch.Generator().manual_seed(6)
+    n = torch.randint(0, 17, (B,), generator=g, dtype=torch.int32)
+    qkv = torch.randn(B, hq + 2 * hkv, d, generator=g).half()
+    kp, vp = (torch.zeros((64, hkv, 10 * d) if q4 else (1024, hkv, d), dtype=torch.uint8 if q4 else torch.float16,
+                          device="cuda") for _ in range(2))
+    slots = torch.full((B,), -1, dtype=torch.int64)
+    at = torch.arange(0, B, 69)[:1000]
+    slots[at] = torch.arange(1000)
+    append, attend = ((lib.paged_kv_append_q4, lib.paged_attn_q4) if q4 else (lib.paged_kv_append, lib.paged_attn_window))
+    dev = qkv.cuda()
+    q = append(dev[:, :hq], dev[:, hq:hq + hkv], dev[:, hq + hkv:], None, None, slots.cuda(), kp, vp)
+    assert torch.equal(q, dev[:, :hq])
+    table = torch.arange(B, dtype=torch.int32)[:, None] % 62
+    out = attend(q, kp, vp, table.cuda(), torch.arange(B + 1, dtype=torch.int32).cuda(), n.cuda(), 1, 16, 0.125)
+    if q4:
+        k, v = (torch.from_numpy(sv.q4_load(p.cpu().numpy())).view(64, 16, d) for p in (kp, vp))
+    else:
+        k, v = (p.cpu().double().view(64, 16, d) for p in (kp, vp))
+    x = qkv[:, :hq].double()
+    s = torch.einsum("bhd,bkd->bhk", x, k[table[:, 0].long()]) * 0.125
+    seen = torch.arange(16)[None, None] < n[:, None, None]
+    p = torch.where(seen, s, torch.tensor(-float("inf"))).softmax(-1).nan_to_num(0)
+    w = v[table[:, 0].long()]
+    want, spread = torch.einsum("bhk,bkd->bhd", p, w), torch.einsum("bhk,bkd->bhd", p, w.abs())
+    reach = (torch.einsum("bhd,bkd->bhk", x.abs(), k[table[:, 0].long()].abs()) * 0.125).amax(-1)
+    agree(out.double().cpu().numpy(), want.numpy(),
+          sc.tolerance(want.numpy(), spread.numpy(), reach.numpy(), 16, d, "f16", 2.0 ** -11))

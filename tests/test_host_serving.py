@@ -248,3 +248,24 @@ def test_fast_append_makes_the_call(fast):
 ])
 def test_fast_append_leaves_the_rest_alone(fast, change):
     assert fast.append(*fast_append(**change)) is None
+
+
+def test_scratch_is_allocated_on_the_calls_stream(monkeypatch):
+    """Memory of the current stream could still be in use by work queued there."""
+    import contextlib
+    import types
+    active, made = [None], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        active.append(stream)
+        yield
+        active.pop()
+
+    fake = types.SimpleNamespace(cuda=types.SimpleNamespace(stream=on),
+                                 empty=lambda n, dtype, device: made.append((n, active[-1])))
+    monkeypatch.setattr(lib, "_torch", lambda: fake)
+    q = types.SimpleNamespace(device="cuda:0")
+    lib._scratch(64, q, "side")
+    lib._scratch(32, q, None)
+    assert made == [(64, "side"), (32, None)]
