@@ -325,7 +325,7 @@ PKV_API pkv_status paged_kv_gather_q4(const void* key_pool, const void* value_po
  *   softmax_scale  finite; > 0 for bf16/f16 unless flags holds PKV_FORCE_SIMT
  *   flags          PKV_CHECK_BOUNDS (bad block ids, query lengths, key lengths past the table or max_seq_len),
  *                  PKV_FORCE_SIMT (the fp32 CUDA-core kernel); others are ignored
- * Everything else as paged_attn_varlen; max_query_len may exceed max_seq_len.
+ * Everything else as paged_attn_varlen; max_query_len may exceed max_seq_len, and max_seq_len is at most 2^31 - 256.
  */
 PKV_API pkv_status paged_attn_window(const void* q, int64_t Tq, int Hq, const void* key_pool, const void* value_pool,
                                      int64_t num_blocks, int block_size, int Hkv, int D, pkv_dtype dt,

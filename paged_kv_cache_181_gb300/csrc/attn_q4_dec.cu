@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
   const int key = key_of(gl);
   // Pages [v_lo, v_hi) of the list hold keys that every row sees (besides whole sink pages, which take the masked way).
   int v_lo = 0, v_hi = p_first + 1 > 0 ? (p_first + 1) >> 4 : 0;  // as logical pages
-  if (a.window && p_last - (a.window - 1) > 0) v_lo = (p_last - (a.window - 1) + 15) >> 4;
+  if (a.window && p_last >= a.window) v_lo = (p_last - (a.window - 1) + 15) >> 4;
   v_lo += pg.n_sink - pg.first, v_hi += pg.n_sink - pg.first;
   if (v_lo < pg.n_sink) v_lo = pg.n_sink;
   for (int i = 0; i < n; i += kPG) {

@@ -26,7 +26,7 @@ PKV_DEVINLINE WinPages win_pages(int p_first, int p_last, int window, int sinks)
   WinPages w;
   w.hi = p_last + 1;
   w.lo = 0;
-  if (window > 0 && p_first - (window - 1) > 0) w.lo = p_first - (window - 1);
+  if (window > 0 && p_first >= window) w.lo = p_first - (window - 1);
   w.sinks = sinks < w.hi ? sinks : w.hi;
   const int end = w.hi > 0 ? (w.hi + 15) >> 4 : 0;
   w.first = w.lo >> 4;
@@ -55,7 +55,7 @@ PKV_DEVINLINE WinRow win_row(const PkvWinArgs& a, int b, bool flag) {
       if (flag) pkv_raise(a.err, PKV_DEVERR_QUERY);
       r.Sq = r.Sq < 0 ? 0 : a.max_query_len;
     }
-    const int most = a.W * 16 < a.max_seq_len ? a.W * 16 : a.max_seq_len;
+    const int most = (int64_t)a.W * 16 < a.max_seq_len ? a.W * 16 : a.max_seq_len;
     if (r.L < 0 || r.L > most) {
       if (flag) pkv_raise(a.err, PKV_DEVERR_SEQLEN);
       r.L = r.L < 0 ? 0 : most;

@@ -10,6 +10,7 @@ namespace {
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int kMaxKeys = 0x7fffff00;  // positions of a whole tile past them still fit an int
 
 pkv_status check_dtype(const char* fn, pkv_dtype dt) {
   if (dt == PKV_F32 || dt == PKV_BF16 || dt == PKV_F16) return PKV_OK;
@@ -94,6 +95,8 @@ pkv_status win_impl(const char* fn, bool q4, const void* q, int64_t Tq, int Hq, 
   if ((int64_t)max_seq_len > (int64_t)W * block_size)
     return pkv_fail(PKV_ERR_INVALID_ARG, "%s: max_seq_len %d exceeds the table's %d x %d slots", fn, max_seq_len, W,
                     block_size);
+  if (max_seq_len > kMaxKeys)
+    return pkv_fail(PKV_ERR_UNSUPPORTED, "%s: max_seq_len %d is past the %d keys of one call", fn, max_seq_len, kMaxKeys);
   if (Tq > kMaxGrid || (int64_t)max_query_len * (Hq / Hkv) > kMaxGrid - 1024)
     return pkv_fail(PKV_ERR_UNSUPPORTED, "%s: too many queries for one call", fn);
   if (Tq == 0 || B == 0 || max_query_len == 0) return PKV_OK;
@@ -353,7 +356,7 @@ extern "C" pkv_status paged_kv_gather_q4(const void* key_pool, const void* value
 extern "C" size_t paged_attn_window_workspace_size(int64_t num_blocks, int Hq, int Hkv, int D, pkv_dtype dt, int q4, int B,
                                                    int max_query_len, int max_seq_len, int window, int sinks) {
   if (num_blocks <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || B <= 0 || max_query_len <= 0 || max_seq_len < 0 ||
-      window < 0 || sinks < 0 || (D != 64 && D != 128) || (int64_t)max_query_len * (Hq / Hkv) > kMaxGrid - 1024 ||
+      max_seq_len > kMaxKeys || window < 0 || sinks < 0 || (D != 64 && D != 128) || (int64_t)max_query_len * (Hq / Hkv) > kMaxGrid - 1024 ||
       (dt != PKV_BF16 && dt != PKV_F16) || win_kernel(dt, num_blocks, max_query_len, Hq / Hkv, 0) != WinKernel::kDec)
     return 0;
   PkvWinArgs a{};

@@ -595,3 +595,17 @@ def test_seventy_thousand_sequences(lib, q4):
     reach = (torch.einsum("bhd,bkd->bhk", x.abs(), k[table[:, 0].long()].abs()) * 0.125).amax(-1)
     agree(out.double().cpu().numpy(), want.numpy(),
           sc.tolerance(want.numpy(), spread.numpy(), reach.numpy(), 16, d, "f16", 2.0 ** -11))
+
+
+@pytest.mark.parametrize("dtype,q4,flags", PATHS, ids=lambda v: str(v))
+@pytest.mark.parametrize("rows", [[(90, 60), (2, 40)], [(9, 7), (1, 5)]], ids=["prompt", "few"])
+def test_widest_window_with_queries_before_the_keys(lib, rows, dtype, q4, flags):
+    """A window as large as the type allows, and rows whose first queries see no key."""
+    agree(*attention(lib, rows, 4, 2, 64, dtype, 2 ** 31 - 1, 2, q4, seed=8, flags=flags))
+
+
+@pytest.mark.parametrize("q4,dtype", [(False, "bf16"), (True, "f16"), (False, "f32")])
+@pytest.mark.parametrize("group", [128, 160])
+def test_heads_that_fill_or_pass_a_tile(lib, group, q4, dtype):
+    """128 query heads a kv head are a whole tile for each token; more take the few-rows kernel at every length."""
+    agree(*attention(lib, [(5, 90), (1, 33), (40, 40)], group, 1, 64, dtype, 30, 1, q4, seed=group))

@@ -69,6 +69,7 @@ def attn(name="paged_attn_window", q=P, Tq=4, hq=4, kp=P, vp=P, nblk=8, bs=16, h
     (dict(ws=P + 8), lib.PKV_ERR_INVALID_ARG, "workspace"),
     (dict(nblk=0), lib.PKV_ERR_INVALID_ARG, "without blocks"),
     (dict(mq=2 ** 31 - 1), lib.PKV_ERR_UNSUPPORTED, "too many"),
+    (dict(W=2 ** 27, ml=2 ** 31 - 255), lib.PKV_ERR_UNSUPPORTED, "max_seq_len"),
 ])
 def test_attention_refusals(name, change, status, word):
     assert attn(name, **change) == status
