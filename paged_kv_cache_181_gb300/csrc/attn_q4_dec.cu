@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
 template <typename T, int D, int NT>
 int launch_nt(const PkvWinArgs& a, void* ws, size_t bytes, size_t* wanted, int* launches, cudaStream_t s) {
   static PkvKernelState state;
-  return dec::launch<T, D, NT>(attn_q4_dec_kernel<T, D, NT>, state, sizeof(Smem<D, NT>), 0.84, a, ws, bytes, wanted,
+  return dec::launch<T, D, NT>(attn_q4_dec_kernel<T, D, NT>, state, sizeof(Smem<D, NT>), 0.4, 7.0, a, ws, bytes, wanted,
                              launches, s);
 }
 

@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 template <typename T, int D, int NT>
 int launch_nt(const PkvWinArgs& a, void* ws, size_t bytes, size_t* wanted, int* launches, cudaStream_t s) {
   static PkvKernelState state;
-  return dec::launch<T, D, NT>(attn_win_dec_kernel<T, D, NT>, state, sizeof(Smem<D, NT>), 0.95, a, ws, bytes, wanted,
+  return dec::launch<T, D, NT>(attn_win_dec_kernel<T, D, NT>, state, sizeof(Smem<D, NT>), 0.34, 5.2, a, ws, bytes, wanted,
                              launches, s);
 }
 

@@ -312,11 +312,11 @@ int launch_rows(const PkvWinArgs& a, cudaStream_t s) {
     static PkvKernelState state;
     const int64_t keys = pkv_visible_keys(a, a.max_query_len);
     return launch(attn_win_simt_few_kernel<T, Pool, D>, state, sizeof(FewSmem<D>), (int64_t)a.B * a.Hkv,
-                  keys / (8 * kWarps) + 1, 0.8, 2.0, a, s);
+                  keys / (8 * kWarps) + 1, 0.4, 4.7, a, s);
   }
   static PkvKernelState state;
   return launch(attn_win_simt_kernel<T, Pool, D>, state, sizeof(Smem<D>), (int64_t)a.B * a.Hkv * ((rows + kRows - 1) / kRows),
-                pkv_visible_keys(a, kRows / g + 1) / kKeys + 1, 0.4, 0.5, a, s);
+                pkv_visible_keys(a, kRows / g + 1) / kKeys + 1, 0.25, 0.4, a, s);
 }
 
 template <typename T, typename Pool>

@@ -146,8 +146,8 @@ struct PkvKernelState {
 int pkv_prepare_kernel(const void* kernel, int smem, int threads, int regs, PkvKernelState& state);
 // Keys that a tile of `tokens` query tokens can see, from the sizes the host knows.
 int64_t pkv_visible_keys(const PkvWinArgs& a, int64_t tokens);
-// CTAs (1, 2, 4, 8 or 16) that share one item's `steps` key steps; `rate`: what a step costs each of several CTAs on
-// an SM, times their number, as against one alone; `setup`: a CTA's set-up in steps.
+// CTAs (1, 2, 4, 8 or 16) that share one item's `steps` key steps; `rate`: the share of an SM that one CTA needs;
+// `setup`: a CTA's set-up in steps of one that has its SM to itself.
 int pkv_plan_cluster(const PkvKernelState& state, int64_t items, int64_t steps, double rate, double setup);
 constexpr int kPkvMaxWinSplits = 64;
 // Single CTAs (2 .. kPkvMaxWinSplits) that share one item where that is estimated under any cluster; else 1.  `combine`: the cost of

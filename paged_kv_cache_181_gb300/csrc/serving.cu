@@ -188,8 +188,8 @@ struct Split {
   double cost;
 };
 
-// A kernel of one CTA per SM runs in waves of the clusters that fit the GPU at once; each CTA takes its share of the steps plus the
-// fixed cost.  The smallest estimate wins, a larger cluster only where it gains a tenth.
+// A kernel of one CTA per SM runs in waves of the clusters that fit the GPU at once; each CTA takes its share of the
+// steps plus the fixed cost.  The smallest estimate wins, a larger cluster only where it gains a tenth.
 Split best_split(const PkvKernelState& state, int dev, int64_t items, int64_t steps, double fixed) {
   Split best{1, 1e300};
   for (int i = 0; i < 5; ++i) {
@@ -212,20 +212,22 @@ int current_device() {
 
 }  // namespace
 
-// Kernels of several CTAs per SM, in steps of a CTA that has its SM to itself: CTAs that share an SM take turns, each step
-// then costing `rate` (a little under 1: one CTA of four warps nearly takes an SM's share of the memory or of its issue
-// slots by itself), and each CTA costs `setup` steps more.  The SM with the most CTAs decides; past four of them the
-// hardware deals them out as they finish.  A cluster costs its launch and merge.  Fitted to 25 mixes of 1 to 64 sequences,
-// 80 to 50000 keys and 1 to 8 kv heads, timed with every cluster size: the choice is the best of them or within a
-// tenth of it.
+// Kernels of several CTAs per SM, in steps of a CTA that has its SM to itself.  Such a CTA waits for its loads most of
+// the time, so a second one costs nothing at first; `rate` is the share of the SM (its memory bandwidth or its issue
+// slots) that one needs, and from 1 / rate of them on they take turns.  Each CTA costs `setup` steps more, less where
+// others work meanwhile.  The SM with the most CTAs decides; past three of them the hardware deals them out as they
+// finish.  A cluster costs its launch and merge.  Fitted to 681 mixes of 1 to 100 sequences, 73 to 131072 keys, 1 to 8 kv
+// heads, one query to prompts, timed with every cluster size and several splits: the choice is 2 % (16-bit and fp32 tiles),
+// 1 % (4-bit) and 6 % (fp32, few rows) over the best on average; a model whose CTAs share an SM at the rate of one was
+// 14, 11, 3 and 13 % over it.
 static double shared_cost(int64_t ctas, int64_t sms, int64_t steps, double rate, double setup) {
   const double k = (double)ctas / (double)sms;
-  const double most = k <= 1.0 ? 1.0 : k <= 4.0 ? ceil(k) : k + 0.7;
-  return most * ((double)steps * (most > 1.0 ? rate : 1.0) + setup);
+  const double most = k <= 1.0 ? 1.0 : k <= 3.0 ? ceil(k) : k + 1.1;
+  return (most * rate > 1.0 ? most * rate : 1.0) * (double)steps + setup * (1.0 + 0.31 * (most - 1.0));
 }
 
 static Split best_cluster(const PkvKernelState& state, int dev, int64_t items, int64_t steps, double rate, double setup) {
-  static const double merge[5] = {0.0, 0.65, 0.75, 1.0, 2.5};  // in set-ups
+  static const double merge[5] = {0.0, 0.56, 0.55, 0.63, 1.33};  // in set-ups
   const int64_t sms = pkv_sm_count() > 0 ? pkv_sm_count() : 152;
   Split best{1, 1e300};
   for (int i = 0; i < 5; ++i) {

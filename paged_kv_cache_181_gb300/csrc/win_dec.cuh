@@ -12,9 +12,9 @@ namespace dec {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr float kRescale = 8.f;  // log2 units
-// What a CTA's set-up costs and what the combine launch has to gain, in steps (one page per warp): 3 us on the GPU, and
-// 8 us of the host's time (a workspace, a launch), which a stream of short calls waits for.
-constexpr double kSetupSteps = 2.0, kCombineSteps = 8.0;
+// What the combine launch has to gain, in steps (one page per warp): 3 us on the GPU, and 8 us of the host's time (a
+// workspace, a launch), which a stream of short calls waits for.
+constexpr double kCombineSteps = 12.0;
 
 template <bool BF16>
 PKV_DEVINLINE void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(D) combine_kernel(const PkvWinArgs a, const in
 
 // Plans and launches `kernel`, compiled for tiles of 8 NT rows.  ws_wanted: only say what workspace the call would use.
 template <typename T, int D, int NT, typename Kernel>
-int launch(Kernel kernel, PkvKernelState& state, size_t smem, double rate, const PkvWinArgs& a, void* workspace,
+int launch(Kernel kernel, PkvKernelState& state, size_t smem, double rate, double setup, const PkvWinArgs& a, void* workspace,
            size_t ws_bytes, size_t* ws_wanted, int* launches, cudaStream_t s) {
   int rc = pkv_prepare_kernel((const void*)kernel, (int)smem, kThreads, 0, state);
   if (rc) return rc;
@@ -279,7 +279,7 @@ int launch(Kernel kernel, PkvKernelState& state, size_t smem, double rate, const
   const int64_t items = (int64_t)a.B * a.Hkv * (((int64_t)a.max_query_len * g + 8 * NT - 1) / (8 * NT));
   const int64_t steps = pkv_visible_keys(a, 8 * NT / g + 1) / (16 * kWarps) + 1;
   // Items too few for clusters of 16 to fill the GPU: more CTAs per item, and the combine launch.
-  int splits = pkv_plan_splits(state, items, steps, rate, kSetupSteps, kCombineSteps);
+  int splits = pkv_plan_splits(state, items, steps, rate, setup, kCombineSteps);
   const size_t need = splits > 1 ? (size_t)(items * splits * kPartialFloats<D, NT> * 4) : 0;
   if (ws_wanted) {
     *ws_wanted = need;
@@ -288,7 +288,7 @@ int launch(Kernel kernel, PkvKernelState& state, size_t smem, double rate, const
   if (need > ws_bytes || !workspace) splits = 1;
   float* ws = splits > 1 ? (float*)workspace : nullptr;
   void* args[] = {const_cast<PkvWinArgs*>(&a), &splits, &ws};
-  const int ctas = splits > 1 ? 1 : pkv_plan_cluster(state, items, steps, rate, kSetupSteps);
+  const int ctas = splits > 1 ? 1 : pkv_plan_cluster(state, items, steps, rate, setup);
   *launches = 1;
   rc = pkv_launch_cluster((const void*)kernel, splits > 1 ? items * splits : items, ctas, kThreads, smem, args, false, s);
   if (rc || splits == 1) return rc;
