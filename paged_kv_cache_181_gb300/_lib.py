@@ -426,7 +426,8 @@ def _init_fast() -> None:
         _current_device = lambda: -2  # noqa: E731  (no tensor is on it)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-    _fastcall.setup((torch.float32, torch.bfloat16, torch.float16), _u8, _i32t, _i64, _current_device, _raw_stream)
+    _fastcall.setup((torch.float32, torch.bfloat16, torch.float16), _u8, _i32t, _i64, _current_device, _raw_stream,
+                    _scratch)
 
 
 def _code(fn: str, dtype) -> int:
@@ -690,11 +691,8 @@ def paged_attn_window(q, key_pool, value_pool, block_table, query_start_loc, seq
     """
     if out is None:
         out = _torch().empty_like(q)
-    args = (False, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len, max_seq_len,
-            softmax_scale, window, sinks, out)
-    status = _fastcall.attend(*args, workspace, flags, block_size, stream)
-    if status is not None and status < 0:
-        status = _fastcall.attend(*args, _scratch(-status, q, stream), flags, block_size, stream)
+    status = _fastcall.attend(False, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len,
+                              max_seq_len, softmax_scale, window, sinks, out, workspace, flags, block_size, stream)
     if status is not None:
         if status:
             _ok(status)
@@ -710,11 +708,8 @@ def paged_attn_q4(q, key_pool, value_pool, block_table, query_start_loc, seq_len
     """paged_attn_window over 4-bit pools (uint8 ``[num_blocks, Hkv, q4_block_bytes(D)]``); returns ``out``."""
     if out is None:
         out = _torch().empty_like(q)
-    args = (True, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len, max_seq_len,
-            softmax_scale, window, sinks, out)
-    status = _fastcall.attend(*args, workspace, flags, block_size, stream)
-    if status is not None and status < 0:
-        status = _fastcall.attend(*args, _scratch(-status, q, stream), flags, block_size, stream)
+    status = _fastcall.attend(True, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len,
+                              max_seq_len, softmax_scale, window, sinks, out, workspace, flags, block_size, stream)
     if status is not None:
         if status:
             _ok(status)

@@ -17,7 +17,7 @@
 
 static PyObject *s_data_ptr, *s_get_device, *s_is_contiguous, *s_dtype, *s_shape, *s_stride, *s_cuda_stream, *s_nbytes;
 static PyObject *dt_code[3], *dt_u8, *dt_i32, *dt_i64; /* dt_code: by pkv_dtype */
-static PyObject *current_device, *raw_stream;
+static PyObject *current_device, *raw_stream, *scratch;
 
 typedef struct {
   PyObject* shape; /* new reference */
@@ -109,8 +109,7 @@ static PyObject* decline(void) {
   Py_RETURN_NONE;
 }
 
-/* -n: nothing was done, the call wants a workspace of n bytes.
- * attend(q4, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len, max_seq_len, scale, window,
+/* attend(q4, q, key_pool, value_pool, block_table, query_start_loc, seq_lens, max_query_len, max_seq_len, scale, window,
  *        sinks, out, workspace, flags, block_size, stream) */
 static PyObject* attend(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
@@ -123,7 +122,7 @@ static PyObject* attend(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   PyObject* const objs[8] = {a[1], a[2], a[3], a[4], a[5], a[6], a[12], a[13]};
   const int count = a[13] == Py_None ? 7 : 8;
   int loaded = 0, status = -1;
-  size_t wanted = 0;
+  PyObject* owned = NULL; /* a workspace of this call */
   for (; loaded < count; ++loaded)
     if (!load(objs[loaded], dev, 0, &t[loaded])) {
       ++loaded;
@@ -161,9 +160,17 @@ static PyObject* attend(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       ws = t[7].ptr;
     } else if (B * hkv < 256 && code && ml > 1024 && (window > 1024 || window == 0)) {
       /* Few sequences and heads over many keys: no other sizes take a workspace. */
-      wanted = paged_attn_window_workspace_size(blocks, (int)hq, (int)hkv, (int)d, (pkv_dtype)code, q4, (int)B, mq, ml,
-                                                window, sinks);
-      if (wanted) goto done;
+      ws_bytes = (long long)paged_attn_window_workspace_size(blocks, (int)hq, (int)hkv, (int)d, (pkv_dtype)code, q4,
+                                                             (int)B, mq, ml, window, sinks);
+      if (ws_bytes) {
+        PyObject* size = scratch ? PyLong_FromLongLong(ws_bytes) : NULL;
+        long long at;
+        if (!size) goto done;
+        owned = PyObject_CallFunctionObjArgs(scratch, size, a[1], a[16], NULL);
+        Py_DECREF(size);
+        if (!owned || !method_long(owned, s_data_ptr, &at)) goto done;
+        ws = (void*)(intptr_t)at;
+      }
     }
     void* stream;
     if (!stream_of(a[16], devo, &stream)) goto done;
@@ -175,7 +182,7 @@ static PyObject* attend(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 done:
   drop(t, loaded);
   Py_DECREF(devo);
-  if (wanted) return PyLong_FromLongLong(-(long long)wanted);
+  Py_XDECREF(owned); /* torch's allocator keeps the memory for this stream's order */
   return status < 0 ? decline() : PyLong_FromLong(status);
 }
 
@@ -265,11 +272,11 @@ done:
   return status < 0 ? decline() : PyLong_FromLong(status);
 }
 
-/* setup((f32, bf16, f16), uint8, int32, int64, current_device, raw_stream) */
+/* setup((f32, bf16, f16), uint8, int32, int64, current_device, raw_stream[, scratch]) */
 static PyObject* setup(PyObject* self, PyObject* args) {
   (void)self;
-  PyObject *f32, *bf16, *f16, *u8, *i32, *i64, *cur, *raw;
-  if (!PyArg_ParseTuple(args, "(OOO)OOOOO", &f32, &bf16, &f16, &u8, &i32, &i64, &cur, &raw)) return NULL;
+  PyObject *f32, *bf16, *f16, *u8, *i32, *i64, *cur, *raw, *mem = NULL;
+  if (!PyArg_ParseTuple(args, "(OOO)OOOOO|O", &f32, &bf16, &f16, &u8, &i32, &i64, &cur, &raw, &mem)) return NULL;
   PyObject* const v[8] = {f32, bf16, f16, u8, i32, i64, cur, raw};
   PyObject** const to[8] = {&dt_code[PKV_F32], &dt_code[PKV_BF16], &dt_code[PKV_F16], &dt_u8, &dt_i32, &dt_i64,
                             &current_device, &raw_stream};
@@ -277,6 +284,8 @@ static PyObject* setup(PyObject* self, PyObject* args) {
     Py_INCREF(v[i]);
     Py_XSETREF(*to[i], v[i]);
   }
+  Py_XINCREF(mem);
+  Py_XSETREF(scratch, mem);
   Py_RETURN_NONE;
 }
 
@@ -284,7 +293,7 @@ static PyMethodDef methods[] = {
     {"attend", (PyCFunction)(void (*)(void))attend, METH_FASTCALL, "paged_attn_window / paged_attn_q4"},
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, "paged_kv_append / paged_kv_append_q4"},
     {"gather", (PyCFunction)(void (*)(void))gather, METH_FASTCALL, "paged_kv_gather_q4"},
-    {"setup", setup, METH_VARARGS, "dtypes and torch's device and stream queries"},
+    {"setup", setup, METH_VARARGS, "dtypes, torch's device and stream queries, and the workspace allocation"},
     {NULL, NULL, 0, NULL},
 };
 

@@ -12,9 +12,9 @@ namespace dec {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr float kRescale = 8.f;  // log2 units
-// What the combine launch has to gain, in steps (one page per warp): 3 us on the GPU, and 8 us of the host's time (a
+// What the combine launch has to gain, in steps (one page per warp): 3 us on the GPU, and 6.5 us of the host's time (a
 // workspace, a launch), which a stream of short calls waits for.
-constexpr double kCombineSteps = 12.0;
+constexpr double kCombineSteps = 8.0;
 
 template <bool BF16>
 PKV_DEVINLINE void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
