@@ -7,7 +7,7 @@
 // per key (K rows padded by 16 bytes, so the lanes' float4 reads spread over the banks; Q rows are broadcast reads), an
 // online softmax with the running maximum and sum in registers, then P.V with a lane per D/32 channels.  16 warps an SM
 // hide what each waits for; tiles of 64 keys, two a lane, and register tiles of 8 x 4 scores need fewer reads for an FMA
-// but leave 8 warps, and measured slower (3 sequences, 333 queries, window 501: 72 and 90 us instead of 51).
+// but leave 8 warps, and measured slower (3 sequences, 333 queries, window 501: 72 and 90 us instead of 50).
 
 // Calls of at most 8 rows (decode): bound by memory, so keys and values go from memory to registers.  Half a warp
 // takes a key, a lane D/16 of its channels for every row; four keys at a time, whose scores are summed over the half
