@@ -27,7 +27,9 @@
 // accumulators fill it at D = 128), so each 128 keys take the softmax (1700 cycles; masked ones 2800 and more), its two
 // products (1024 cycles) and the hand-overs one after the other, 3400 cycles, while only the other tile's products fill
 // the gaps: 1.2 PFLOP/s over 4000-key windows, 1.06 with 4-bit pools, where turning codes into numbers adds to it.
-// Scores of 64 keys that go on by themselves were slower (a TMEM read is mostly latency, and there were twice as many).
+// Scores of 64 keys that go on by themselves were slower (a TMEM read is mostly latency, and there were twice as many),
+// and so were two threads a row (the maxima have to be exchanged: 165 us for two prompts of up to 4096 tokens with a
+// window of 1024, against 142).
 // The order of MMAs, the ring of slots shared by key and value tiles, the lazy rescale and the register split between
 // warpgroups are those of the prefix-mask kernel (attn_tc.cu), which says why.
 // Every mbarrier wait is bounded in time (1 s, or 60 for the next item); on expiry the CTA records PKV_DEVERR_TIMEOUT
@@ -99,7 +101,7 @@ struct alignas(1024) WinSmem {
   uint64_t full[C::NSLOT], empty[C::NSLOT];
   uint64_t raw_full[3], raw_empty[3];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];  // p_full: [query tile][part of the keys]
-  uint64_t info_full[2], info_empty[2], clc_full;
+  uint64_t info_full[2], info_empty[2], clc_full, tile_sync[2];
   alignas(16) uint4 clc;  // the scheduler's last answer
   Item info[2];           // the item in work, and the one to come
   uint32_t tmem_base;
@@ -297,6 +299,7 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
       ptx::mbar_init(&sm.info_empty[w], kReaders);
     }
     ptx::mbar_init(&sm.clc_full, 1);
+    for (int w = 0; w < 2; ++w) ptx::mbar_init(&sm.tile_sync[w], 4);
     sm.abort = 0;
     // After a pipeline timeout in an earlier launch results are invalid: do not wait for it again.
     sm.skip = (*(volatile unsigned int*)a.err & PKV_DEVERR_TIMEOUT) != 0;
@@ -705,6 +708,13 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
       ptx::mbar_arrive(&sm.empty[staged]);
       staged = -1;
     };
+    // All warps of the tile; on an mbarrier, because a warp that gave up elsewhere does not come.
+    int syncs = 0;
+    auto tile_sync = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sm.tile_sync[grp]);
+      return __all_sync(0xffffffffu, ptx::mbar_wait(&sm.tile_sync[grp], syncs++ & 1, &sm.abort, kWaitLimitNs));
+    };
     while (next_item()) {
       const Item& it = sm.info[seq & 1];
       // (The item is read from shared memory where it is used: the scores need the registers.)
@@ -940,8 +950,8 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
             const int first = it.i0 + grp * TM;
             if (first + TM <= it.Sq) {  // whole tiles: one TMA store per column half
               ptx::fence_proxy_async_smem();
-              asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(BM) : "memory");
-              if (trow == 0) {
+              ok = tile_sync();
+              if (ok && trow == 0) {
 #pragma unroll
                 for (int dh = 0; dh < D / 64; ++dh)
                   tma_store_4d(&maps.o, dh * 64, 0, it.kvh, it.q0 + first, tile + dh * (BM * 128));
@@ -949,15 +959,19 @@ __global__ void __launch_bounds__(Roles<POOLQ4>::kThreads, 1)
                 staged = slot;  // given back once it has been read: when the next item's first scores are there
               }
             } else {  // a sequence's last tile: the rows that are queries
-              asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(BM) : "memory");
-              const int rows = (it.Sq - first) * g;
+              ok = tile_sync();
+              const int rows = ok ? (it.Sq - first) * g : 0;
               for (int e = trow; e < rows * (D / 8); e += BM) {
                 const int r = e / (D / 8), v = e % (D / 8);
                 reinterpret_cast<uint4*>(out + ((int64_t)(first + r / g) * a.Hq + r % g) * D)[v] =
                     *reinterpret_cast<const uint4*>(tile + (v >> 3) * (BM * 128) + r * 128 + (((v & 7) ^ (r & 7)) << 4));
               }
-              asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(BM) : "memory");
-              if (trow == 0) ptx::mbar_arrive(&sm.empty[slot]);
+              ok = ok && tile_sync();
+              if (ok && trow == 0) ptx::mbar_arrive(&sm.empty[slot]);
+            }
+            if (!ok) {
+              note_abort(sm, a.err);
+              break;
             }
           } else if (valid) {
             uint4* dst = reinterpret_cast<uint4*>(out + ((int64_t)tok * a.Hq + trow % g) * D);
