@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
     if (!all) {
 #pragma unroll
       for (int u = 0; u < kPG; ++u) {
-        const int j0 = i + u < n ? pg.page(v + u * stride) * 16 : 0x3ffffff0;
+        const int j0 = i + u < n ? pg.page(v + u * stride) * 16 : 0x7fffff00;  // past every key
         seen[u] = __ballot_sync(0xffffffffu, pg.any(j0 + (lane & 15))) & 0xffffu;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)

@@ -609,3 +609,64 @@ def test_widest_window_with_queries_before_the_keys(lib, rows, dtype, q4, flags)
 def test_heads_that_fill_or_pass_a_tile(lib, group, q4, dtype):
     """128 query heads a kv head are a whole tile for each token; more take the few-rows kernel at every length."""
     agree(*attention(lib, [(5, 90), (1, 33), (40, 40)], group, 1, 64, dtype, 30, 1, q4, seed=group))
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_two_billion_keys(lib, q4):
+    """The longest sequence a call takes (its table repeats four blocks): the answer is that of the four."""
+    n, hq, d = 2 ** 31 - 256, 8, 64
+    g = torch.Generator().manual_seed(4)
+    if q4:
+        kn, vn = (sc.random_q4_pool(4, 1, d, s) for s in (1, 2))
+        kp, vp, k, v = torch.from_numpy(kn).cuda(), torch.from_numpy(vn).cuda(), sv.q4_load(kn), sv.q4_load(vn)
+    else:
+        kp, vp = (torch.randn(64, 1, d, generator=g).bfloat16().cuda() for _ in range(2))
+        k, v = kp.cpu().double().numpy(), vp.cpu().double().numpy()
+    q = torch.randn(1, hq, d, generator=g).bfloat16().cuda()
+    table = (torch.arange(n // 16, device="cuda", dtype=torch.int32) % 4)[None]
+    fn = lib.paged_attn_q4 if q4 else lib.paged_attn_window
+    out = fn(q, kp, vp, table, torch.tensor([0, 1], dtype=torch.int32).cuda(), torch.tensor([n], dtype=torch.int32).cuda(),
+             1, n, 0.125, flags=lib.PKV_CHECK_BOUNDS)
+    assert lib.check() == 0
+    want, spread, reach = sv.window_attention(q.cpu().double().numpy(), k, v, np.arange(4)[None], [0, 1], [64], 0.125, 0, 0)
+    # Sums in fp32 run over the keys of one lane (at most n / (64 CTAs x 4 warps x 8 lanes) roundings of a sum, and the
+    # merges of 64 x 32 of them), in place of the four blocks' 64.
+    agree(out.double().cpu().numpy(), want, sc.tolerance(want, spread, reach, n // 2048 + 2048, d, "bf16", 2.0 ** -8))
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_captured_calls_keep_their_own_scratch(lib, q4):
+    """Two graphs of calls that split their keys over a workspace of the binding's, replayed at the same time."""
+    n, d = 32768, 64
+    size = lib.window_workspace_size(n // 16, 4, 1, d, torch.bfloat16, 1, 1, n, 0, 0, q4)
+    assert size > 0
+    g = torch.Generator().manual_seed(3)
+    if q4:
+        kp, vp = (torch.from_numpy(sc.random_q4_pool(n // 16, 1, d, s)).cuda() for s in (1, 2))
+    else:
+        kp, vp = (torch.randn(n, 1, d, generator=g).bfloat16().cuda() for _ in range(2))
+    meta = (torch.arange(n // 16, dtype=torch.int32)[None].cuda(), torch.tensor([0, 1], dtype=torch.int32).cuda(),
+            torch.tensor([n], dtype=torch.int32).cuda(), 1, n, 0.125)
+    fn = lib.paged_attn_q4 if q4 else lib.paged_attn_window
+    qs = [torch.randn(1, 4, d, generator=g).bfloat16().cuda() for _ in range(2)]
+    want = [fn(q, kp, vp, *meta) for q in qs]
+    assert lib.last_launches() == 2
+    graphs, outs = [], [[torch.zeros_like(q) for _ in range(4)] for q in qs]
+    for q, out in zip(qs, outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for o in out:
+                fn(q, kp, vp, *meta, out=o)
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(5):
+        for out in outs:
+            for o in out:
+                o.zero_()
+        torch.cuda.synchronize()
+        for st, graph in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+        for out, w in zip(outs, want):
+            assert all(torch.equal(o, w) for o in out)
