@@ -670,3 +670,42 @@ def test_captured_calls_keep_their_own_scratch(lib, q4):
         torch.cuda.synchronize()
         for out, w in zip(outs, want):
             assert all(torch.equal(o, w) for o in out)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_captured_prompts_on_two_streams(lib, q4):
+    """Prompt calls of one launch and of two (whole waves, and clusters for the rest), captured and replayed at once."""
+    d, hkv, n = 128, 8, 8192
+    g = torch.Generator().manual_seed(13)
+    if q4:
+        kp, vp = (torch.randint(0, 50, (n // 16, hkv, 10 * d), generator=g, dtype=torch.uint8).cuda() for _ in range(2))
+    else:
+        kp, vp = (torch.randn(n, hkv, d, generator=g).bfloat16().cuda() for _ in range(2))
+    table = torch.randperm(n // 16, generator=g).int()[None].cuda()
+    fn = lib.paged_attn_q4 if q4 else lib.paged_attn_window
+    calls, inputs = [], []
+    for tokens, hq, window, launches in ((2048, 40, 0, 2), (300, 16, 700, 1)):
+        q = torch.randn(tokens, hq, d, generator=g).bfloat16().cuda()
+        meta = (torch.tensor([0, tokens], dtype=torch.int32).cuda(), torch.tensor([n], dtype=torch.int32).cuda(), tokens, n)
+        run = lambda out, q=q, meta=meta, window=window: fn(q, kp, vp, table, *meta, 0.09, window=window, out=out,  # noqa: E731
+                                                                  flags=lib.PKV_CHECK_BOUNDS)
+        want = run(None)
+        assert lib.last_launches() == launches and want.isfinite().all()
+        graph, outs = torch.cuda.CUDAGraph(), [torch.zeros_like(q) for _ in range(3)]
+        with torch.cuda.graph(graph):
+            for o in outs:
+                run(o)
+        calls.append((graph, outs, want))
+        inputs.append((q, meta))  # a graph reads them where they are: they have to live as long as it does
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(3):
+        for _, outs, _ in calls:
+            for o in outs:
+                o.zero_()
+        torch.cuda.synchronize()
+        for st, (graph, _, _) in zip(streams, calls):
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for _, outs, want in calls for o in outs)
+    assert lib.check() == 0
