@@ -2,8 +2,8 @@
 // way, into 4-bit records; and the read-back of 4-bit blocks into staging buffers.
 //
 // All three are bound by memory: the append reads (Hq + 2 Hkv) D values a token and writes as many (Q and K rotated,
-// V as it is), with about one operation per byte.  8192 tokens, 40 heads over 8 kv heads, D = 128, bf16: 41 us, 85 % of
-// the measured copy bandwidth; into 4-bit records and read back from them 55 us, 69 %; one token 2.7 us, a launch.
+// V as it is), with about one operation per byte.  8192 tokens, 40 heads over 8 kv heads, D = 128, bf16: 38.7 us, 91 %
+// of the measured copy bandwidth; into 4-bit records and read back from them 52.8 us, 72 %; one token 2.7 us, a launch.
 //
 // A thread takes two vectors of 8 channels that the rotation pairs (rot_dim/2 apart) or, where it does not, two
 // others, and keeps their cosines and sines in registers while it walks over the heads of its token, loading four
@@ -118,9 +118,13 @@ struct Raw {
 };
 
 // Block: one token; of its HG groups of D/16 threads each walks every HG-th head.
+// Heads whose loads a thread has in flight (NH), and threads an SM, measured at 8192 tokens, 40/8 heads.  16-bit pools: 4
+// heads, 704 threads 38.7 us (640: 42.0, 768: 39.5, 896: 45.5; 2 heads 40.7).  4-bit ones, which compute longer, with their
+// read-back: 2 heads 52.8 us, 4 heads 55.7.
 template <typename T, int D, bool Q4POOL, int HG>
-__global__ void __launch_bounds__(D / 16 * HG) append_pairs_kernel(const PkvAppendArgs a) {
-  constexpr int U = D / 16, NH = sizeof(T) == 4 ? 2 : 4;
+__global__ void __launch_bounds__(D / 16 * HG, sizeof(T) == 2 && !Q4POOL && HG == 8 ? 704 / (D / 16 * HG) : 0)
+    append_pairs_kernel(const PkvAppendArgs a) {
+  constexpr int U = D / 16, NH = sizeof(T) == 4 || (Q4POOL && HG == 8) ? 2 : 4;
   const int64_t t = blockIdx.x;
   const int u = threadIdx.x % U, hg = threadIdx.x / U;
   const int64_t slot = a.slots[t];
