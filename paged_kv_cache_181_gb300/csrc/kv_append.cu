@@ -3,7 +3,7 @@
 //
 // All three are bound by memory: the append reads (Hq + 2 Hkv) D values a token and writes as many (Q and K rotated,
 // V as it is), with about one operation per byte.  8192 tokens, 40 heads over 8 kv heads, D = 128, bf16: 38.7 us, 91 %
-// of the measured copy bandwidth; into 4-bit records and read back from them 52.8 us, 72 %; one token 2.7 us, a launch.
+// of the measured copy bandwidth; into 4-bit records and read back from them 50.4 us, 76 %; one token 2.7 us, a launch.
 //
 // A thread takes two vectors of 8 channels that the rotation pairs (rot_dim/2 apart) or, where it does not, two
 // others, and keeps their cosines and sines in registers while it walks over the heads of its token, loading four
@@ -118,13 +118,15 @@ struct Raw {
 };
 
 // Block: one token; of its HG groups of D/16 threads each walks every HG-th head.
-// Heads whose loads a thread has in flight (NH), and threads an SM, measured at 8192 tokens, 40/8 heads.  16-bit pools: 4
-// heads, 704 threads 38.7 us (640: 42.0, 768: 39.5, 896: 45.5; 2 heads 40.7).  4-bit ones, which compute longer, with their
-// read-back: 2 heads 52.8 us, 4 heads 55.7.
+// Heads that a thread loads at once (NH), whether it loads the next ones before it works on these (AHEAD), and threads an
+// SM, measured at 8192 tokens, 40/8 heads.  16-bit pools: 4 heads, 704 threads 38.6 us (640: 42.0, 768: 39.5, 896: 45.5;
+// 2 heads 40.7, ahead 39.1).  4-bit ones, which compute longer, with their read-back: 2 heads ahead, 832 threads 50.4 us (not
+// ahead 52.8, 4 heads 55.7).
 template <typename T, int D, bool Q4POOL, int HG>
-__global__ void __launch_bounds__(D / 16 * HG, sizeof(T) == 2 && !Q4POOL && HG == 8 ? 704 / (D / 16 * HG) : 0)
+__global__ void __launch_bounds__(D / 16 * HG, sizeof(T) == 2 && HG == 8 ? (Q4POOL ? 832 : 704) / (D / 16 * HG) : 0)
     append_pairs_kernel(const PkvAppendArgs a) {
-  constexpr int U = D / 16, NH = sizeof(T) == 4 || (Q4POOL && HG == 8) ? 2 : 4;
+  constexpr bool AHEAD = Q4POOL && HG == 8;
+  constexpr int U = D / 16, NH = sizeof(T) == 4 || AHEAD ? 2 : 4;
   const int64_t t = blockIdx.x;
   const int u = threadIdx.x % U, hg = threadIdx.x / U;
   const int64_t slot = a.slots[t];
@@ -178,18 +180,26 @@ __global__ void __launch_bounds__(D / 16 * HG, sizeof(T) == 2 && !Q4POOL && HG =
   const T* const q = (const T*)a.q + t * a.q_stride;
   const T* const k = (const T*)a.k + t * a.k_stride;
   const T* const v = (const T*)a.v + t * a.v_stride;
-  for (int h0 = hg; h0 < stop; h0 += NH * HG) {
-    Raw<T> r0[NH], r1[NH];
+  Raw<T> r0[NH], r1[NH];
+  auto fetch = [&](int h0, Raw<T>(&to0)[NH], Raw<T>(&to1)[NH]) {
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
       const int h = h0 + i * HG;
       if (h < stop) {
         const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
         const T* src = is_q ? q + (int64_t)h * D : is_v ? v + (int64_t)(h - a.Hq - a.Hkv) * D : k + (int64_t)(h - a.Hq) * D;
-        r0[i].load(src + 8 * (is_v ? w0 : v0));
-        r1[i].load(src + 8 * (is_v ? w1 : v1));
+        to0[i].load(src + 8 * (is_v ? w0 : v0));
+        to1[i].load(src + 8 * (is_v ? w1 : v1));
       }
     }
+  };
+  if (AHEAD) fetch(hg, r0, r1);
+  for (int h0 = hg; h0 < stop; h0 += NH * HG) {
+    Raw<T> n0[NH], n1[NH];
+    if (AHEAD)
+      fetch(h0 + NH * HG, n0, n1);
+    else
+      fetch(h0, r0, r1);
 #pragma unroll
     for (int i = 0; i < NH; ++i) {
       const int h = h0 + i * HG;
@@ -234,6 +244,10 @@ __global__ void __launch_bounds__(D / 16 * HG, sizeof(T) == 2 && !Q4POOL && HG =
         store8<T>(dst + 8 * o0, x);
         store8<T>(dst + 8 * o1, y);
       }
+    }
+    if (AHEAD) {
+#pragma unroll
+      for (int i = 0; i < NH; ++i) r0[i] = n0[i], r1[i] = n1[i];
     }
   }
 }
