@@ -12,7 +12,7 @@
 // permute per pair makes from two keys' loads.  P^T comes from S^T's registers by one 8x8 transpose per 8 keys.
 // Loads of the next page are issued as soon as the registers of this page's K (then V) are used up: 12 warps of an
 // SM keep 4 to 8 KB each in flight.  64 sequences x 8192-key windows (40/8 heads, D 128): 318 us, 92 % of the measured
-// copy bandwidth; one sequence x 4096 keys, 8 kv heads: 10.7 us, latency (a page's loads, the merge, two launches).
+// copy bandwidth; one sequence x 4096 keys, 8 kv heads: 11 us, latency (a page's loads, the merge, two launches).
 //
 // A row's maximum is raised only when a score exceeds it by 2^8 (one vote per page, no shuffles otherwise);
 // probabilities stay below 2^8, exact in their 16-bit type's range.  P is rounded to the value type for the product,

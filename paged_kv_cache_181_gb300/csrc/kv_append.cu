@@ -2,12 +2,12 @@
 // way, into 4-bit records; and the read-back of 4-bit blocks into staging buffers.
 //
 // All three are bound by memory: the append reads (Hq + 2 Hkv) D values a token and writes as many (Q and K rotated,
-// V as it is), with about one operation per byte.  8192 tokens, 40 heads over 8 kv heads, D = 128, bf16: 38.7 us, 91 %
-// of the measured copy bandwidth; into 4-bit records and read back from them 50.4 us, 76 %; one token 2.7 us, a launch.
+// V as it is), with about one operation per byte.  8192 tokens, 40 heads over 8 kv heads, D = 128, bf16: 38.6 us, 91 %
+// of the measured copy bandwidth; into 4-bit records and read back from them 50.2 us, 76 %; one token 2.7 us, a launch.
 //
 // A thread takes two vectors of 8 channels that the rotation pairs (rot_dim/2 apart) or, where it does not, two
 // others, and keeps their cosines and sines in registers while it walks over the heads of its token, loading four
-// heads' vectors before it uses the first.  In fp32: two products and one sum, each rounded, so that results do not
+// heads' vectors (4-bit pools: two, and the next two meanwhile) before it uses the first.  In fp32: two products and one sum, each rounded, so that results do not
 // depend on how a compiler contracts them.
 //
 // 4-bit pools: the four lanes that hold a group of 32 channels in one of their two vectors find its range with two
