@@ -270,3 +270,23 @@ def test_scratch_is_allocated_on_the_calls_stream(monkeypatch):
     lib._scratch(64, q, "side")
     lib._scratch(32, q, None)
     assert made == [(64, "side"), (32, None)]
+
+
+@pytest.mark.parametrize("source,kernel,variants,spilling,most", [
+    ("attn_win_dec.cu", "attn_win_dec_kernel", 12, "Li128ELi4E", 450),  # 32 rows of 128 channels
+    ("attn_q4_dec.cu", "attn_q4_dec_kernel", 12, "Li128ELi2E", 8),
+    ("attn_win_tc.cu", "attn_win_tc_kernel", 8, "", 300),  # a few words of the roles' bookkeeping, none a row's scores
+])
+def test_serving_kernels_fit_their_registers(source, kernel, variants, spilling, most):
+    """The library built in this tree: a toolchain that allocated otherwise would be slower, not wrong."""
+    import os
+
+    from paged_kv_cache_181_gb300 import build as b
+    log = os.path.join(b.OUT_DIR, source + ".ptxas.txt")
+    if not os.path.exists(log):
+        pytest.skip(f"no ptxas report of {source} in this tree")
+    with open(log) as f:
+        got = b.spills(f.read(), kernel)
+    assert len(got) == variants, got
+    for name, st, ld in got:
+        assert max(st, ld) <= (most if spilling in name else 0), (name, st, ld)
