@@ -63,11 +63,17 @@ pkv_status append_impl(const char* fn, bool q4, const void* q, int64_t q_stride,
 
 enum class WinKernel { kSimt, kTc, kDec };
 
-// Up to 32 query rows per kv head the memory-bound kernel, which reads each key once for all of them; beyond, tiles of
-// 256 rows on tcgen05.
-WinKernel win_kernel(pkv_dtype dt, int64_t num_blocks, int64_t max_query_len, int g, uint32_t flags) {
+// Few query rows per kv head take the memory-bound kernel, which reads each key once for all of them; more, tiles of 256
+// rows on tcgen05.  Where they cross depends on how many (sequence, kv head) pairs there are, because the former spreads
+// the keys of a pair further, and on the former's registers.  Measured with 1 and 6 to 100 sequences, 8 kv heads, us:
+//   16-bit, D 128, 20 rows:        6 x 2000 keys 47 against 24 on tcgen05, 1 x 30000 (1 kv head) 22 against 38
+//   16-bit, D 64, 20 and 40 rows:  24 x 2000 keys 53 against 78, 83 against 79; 1 x 65536 45 against 179, 74 against 179
+//   4-bit, D 128, 30 and 40 rows:  24 x 2000 keys 57 against 66, 83 against 67; 1 x 65536 46 against 137, 71 against 137
+WinKernel win_kernel(pkv_dtype dt, bool q4, int64_t num_blocks, int64_t pairs, int D, int64_t max_query_len, int g,
+                     uint32_t flags) {
   if (dt == PKV_F32 || (flags & PKV_FORCE_SIMT)) return WinKernel::kSimt;
-  return max_query_len * g > 32 && num_blocks > 0 && g <= pkv_win_tc_heads() ? WinKernel::kTc : WinKernel::kDec;
+  const int64_t few = (q4 || D == 64 ? 32 : 16) * (pairs < 16 ? 2 : 1);
+  return max_query_len * g > few && num_blocks > 0 && g <= pkv_win_tc_heads() ? WinKernel::kTc : WinKernel::kDec;
 }
 
 pkv_status win_impl(const char* fn, bool q4, const void* q, int64_t Tq, int Hq, const void* key_pool,
@@ -117,7 +123,7 @@ pkv_status win_impl(const char* fn, bool q4, const void* q, int64_t Tq, int Hq, 
   a.err = pkv_device_error_word();
   if (!a.err) return pkv_fail(PKV_ERR_CUDA, "%s: device error word unavailable", fn);
   int rc, launches = 1;
-  switch (win_kernel(dt, num_blocks, max_query_len, Hq / Hkv, flags)) {
+  switch (win_kernel(dt, q4, num_blocks, (int64_t)B * Hkv, D, max_query_len, Hq / Hkv, flags)) {
     case WinKernel::kSimt: rc = pkv_launch_win_simt(a, dt, D, q4, stream); break;
     case WinKernel::kTc: rc = pkv_launch_win_tc(a, Tq, dt, D, q4, &launches, stream); break;
     default:
@@ -359,7 +365,8 @@ extern "C" size_t paged_attn_window_workspace_size(int64_t num_blocks, int Hq, i
                                                    int max_query_len, int max_seq_len, int window, int sinks) {
   if (num_blocks <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || B <= 0 || max_query_len <= 0 || max_seq_len < 0 ||
       max_seq_len > kMaxKeys || window < 0 || sinks < 0 || (D != 64 && D != 128) || (int64_t)max_query_len * (Hq / Hkv) > kMaxGrid - 1024 ||
-      (dt != PKV_BF16 && dt != PKV_F16) || win_kernel(dt, num_blocks, max_query_len, Hq / Hkv, 0) != WinKernel::kDec)
+      (dt != PKV_BF16 && dt != PKV_F16) ||
+      win_kernel(dt, q4 != 0, num_blocks, (int64_t)B * Hkv, D, max_query_len, Hq / Hkv, 0) != WinKernel::kDec)
     return 0;
   PkvWinArgs a{};
   a.num_blocks = num_blocks, a.B = B, a.Hq = Hq, a.Hkv = Hkv;
