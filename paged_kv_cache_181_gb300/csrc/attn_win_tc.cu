@@ -163,6 +163,14 @@ PKV_DEVINLINE int tile_block(const PkvWinArgs& a, const WinPages& pg, int b, int
   return lane < kPages && v < pg.n ? win_block(a, b, pg.page(v)) : 0;
 }
 
+// Which keys of a page some row sees, a bit each.  (Key by key it took the value loader 2000 to 4600 cycles a tile, more
+// than all that a tile needs else.)
+PKV_DEVINLINE unsigned seen_keys(const WinPages& pg, int page) {
+  const int j0 = page * 16;
+  auto below = [&](int j) { return j <= j0 ? 0u : j - j0 >= 16 ? 0xffffu : (1u << (j - j0)) - 1u; };  // keys under j
+  return below(pg.hi) & (~below(pg.lo) | below(pg.sinks)) & 0xffffu;
+}
+
 // One warp loads a 16-bit key or value tile: pages [8 kt, 8 kt + 8) of the item's list, a lane per page (block `blk`).
 template <int D>
 PKV_DEVINLINE void load_tile(uint8_t* dst, const WinMaps& maps, bool is_v, uint64_t* full, const PkvWinArgs& a,
@@ -171,25 +179,19 @@ PKV_DEVINLINE void load_tile(uint8_t* dst, const WinMaps& maps, bool is_v, uint6
   const bool there = lane < kPages && v < pg.n;
   const int page = there ? pg.page(v) : 0;
   unsigned seen = there ? 0xffffu : 0u;  // rows of the page that some query sees
-  if (is_v) {
-    if (there) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (!pg.any(page * 16 + r)) seen &= ~(1u << r);
-    }
+  if (is_v && there) seen = seen_keys(pg, page);
+  if (is_v && __any_sync(0xffffffffu, lane < kPages && seen != 0xffffu)) {
     // Unseen value rows are zeroed; whole 128-byte rows, so the swizzle does not matter.
-    bool cleared = false;
     for (int k = 0; k < kPages; ++k) {
       const unsigned bits = __shfl_sync(0xffffffffu, seen, k);
       if (bits == 0xffffu) continue;
-      cleared = true;
       for (int e = lane; e < 16 * (D / 64) * 8; e += 32) {
         const int c = e & 7, dh = (e >> 3) % (D / 64), r = (e >> 3) / (D / 64);
         if (!((bits >> r) & 1))
           *reinterpret_cast<uint4*>(dst + row_offset<D>(16 * k + r, dh) + c * 16) = make_uint4(0, 0, 0, 0);
       }
     }
-    if (cleared) ptx::fence_proxy_async_smem();
+    ptx::fence_proxy_async_smem();
     __syncwarp();
   }
   const int rows = __reduce_add_sync(0xffffffffu, __popc(seen));
