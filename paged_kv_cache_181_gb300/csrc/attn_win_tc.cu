@@ -21,15 +21,15 @@
 // CTAs are persistent: warp 0 asks the hardware for a CTA that has not started yet, cancels its launch and takes its
 // item (clusterlaunchcontrol), and the roles go on to it each at its own pace: the producers load the next item's
 // keys and queries while the softmax warps finish the last one.  8192 tokens x 32 heads over 8 kv heads, D = 128, with a
-// window of 64: 46 us instead of 69 with a CTA an item; window 1024: 145 instead of 163.  (Clusters keep to their item.)
+// window of 64: 46 us instead of 69 with a CTA an item; window 1024: 141 instead of 163.  (Clusters keep to their item.)
 //
-// What bounds it: a tile's chain.  Its probabilities overwrite its scores in TMEM (two score and two output
-// accumulators fill it at D = 128), so each 128 keys take the softmax (1700 cycles; masked ones 2800 and more), its two
-// products (1024 cycles) and the hand-overs one after the other, 3400 cycles, while only the other tile's products fill
-// the gaps: 1.2 PFLOP/s over 4000-key windows, 1.06 with 4-bit pools, where turning codes into numbers adds to it.
+// What bounds it: a tile's chain of hand-overs.  Its probabilities overwrite its scores in TMEM (two score and two output
+// accumulators fill it at D = 128), so scores, softmax, products and the barriers between them follow one another, 3300
+// cycles for 128 keys, and only the other tile's work fills the gaps: 1.19 PFLOP/s over 4000-key windows, 0.97 with 4-bit
+// pools.  With work taken out: no exponentials 0 % faster, no products 11 %, no loads 5 %.
 // Scores of 64 keys that go on by themselves were slower (a TMEM read is mostly latency, and there were twice as many),
-// and so were two threads a row (the maxima have to be exchanged: 165 us for two prompts of up to 4096 tokens with a
-// window of 1024, against 142).
+// and so were two threads a row (the maxima have to be exchanged: 147 us for two prompts of up to 4096 tokens with a
+// window of 1024, against 135).
 // The order of MMAs, the ring of slots shared by key and value tiles, the lazy rescale and the register split between
 // warpgroups are those of the prefix-mask kernel (attn_tc.cu), which says why.
 // Every mbarrier wait is bounded in time (1 s, or 60 for the next item); on expiry the CTA records PKV_DEVERR_TIMEOUT

@@ -66,9 +66,9 @@ enum class WinKernel { kSimt, kTc, kDec };
 // Few query rows per kv head take the memory-bound kernel, which reads each key once for all of them; more, tiles of 256
 // rows on tcgen05.  Where they cross depends on how many (sequence, kv head) pairs there are, because the former spreads
 // the keys of a pair further, and on the former's registers.  Measured with 1 and 6 to 100 sequences, 8 kv heads, us:
-//   16-bit, D 128, 20 rows:        6 x 2000 keys 47 against 24 on tcgen05, 1 x 30000 (1 kv head) 22 against 38
-//   16-bit, D 64, 20 and 40 rows:  24 x 2000 keys 53 against 78, 83 against 79; 1 x 65536 45 against 179, 74 against 179
-//   4-bit, D 128, 30 and 40 rows:  24 x 2000 keys 57 against 66, 83 against 67; 1 x 65536 46 against 137, 71 against 137
+//   16-bit, D 128, 20 rows:        6 x 2000 keys 47 against 22 on tcgen05, 1 x 30000 (1 kv head) 22 against 35
+//   16-bit, D 64, 20 and 40 rows:  24 x 2000 keys 52 against 51, 83 against 51; 1 x 65536 43 against 106, 74 against 106
+//   4-bit, D 128, 30 and 40 rows:  24 x 2000 keys 57 against 66, 83 against 67; 1 x 65536 46 against 136, 70 against 137
 WinKernel win_kernel(pkv_dtype dt, bool q4, int64_t num_blocks, int64_t pairs, int D, int64_t max_query_len, int g,
                      uint32_t flags) {
   if (dt == PKV_F32 || (flags & PKV_FORCE_SIMT)) return WinKernel::kSimt;
